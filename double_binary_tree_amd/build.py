@@ -16,8 +16,9 @@ BUILD = os.path.join(ROOT, "_build")
 LIB = os.path.join(PKG, "libemucomm.so")
 ROCM = os.environ.get("ROCM_PATH", "/opt/rocm")
 
-HIP_SOURCES = ["fused.hip", "stepwise.hip", "ll.hip", "xwg.hip", "noalloc.hip", "stream.hip"]
-CXX_SOURCES = ["api.cpp", "plan.cpp", "topology.cpp"]
+HIP_SOURCES = ["fused.hip", "stepwise.hip", "ll.hip", "xwg.hip", "noalloc.hip", "stream.hip",
+               "xent.hip", "balance.hip", "ortho.hip"]
+CXX_SOURCES = ["api.cpp", "plan.cpp", "topology.cpp", "train.cpp"]
 
 HIPCC_FLAGS = [
     "--offload-arch=gfx950", "-O3", "-fPIC", "-std=c++17",

@@ -1,0 +1,261 @@
+// C ABI of the training-step operators: argument checks, then the launches of
+// xent.hip, balance.hip and ortho.hip.  No state: device memory is the caller's.
+#include "train.h"
+
+#include <hip/hip_runtime_api.h>
+
+#include <algorithm>
+#include <cmath>
+#include <vector>
+
+namespace emu {
+namespace {
+
+bool float_type(int dtype) { return dtype == EMU_FLOAT32 || dtype == EMU_FLOAT16 || dtype == EMU_BFLOAT16; }
+bool valid_ranks(int n) { return n >= 1 && n <= kMaxRanks; }
+bool usable(const void* p) { return p && (uintptr_t)p % kVecBytes == 0; }
+
+// CUs of the current device; an MI355X's without one, so that workspace sizes
+// and argument checks need no GPU (a launch then fails by itself).
+int current_cus() {
+  int dev = 0, cus = 0;
+  if (hipGetDevice(&dev) != hipSuccess ||
+      hipDeviceGetAttribute(&cus, hipDeviceAttributeMultiprocessorCount, dev) != hipSuccess || cus <= 0)
+    return 256;
+  return cus;
+}
+
+// The buffers of a call: an output overlaps nothing else.
+struct Spans {
+  struct Span { uintptr_t lo, hi; bool out; };
+  std::vector<Span> all;
+  void in(const void* p, uint64_t bytes) { if (bytes) all.push_back({(uintptr_t)p, (uintptr_t)p + bytes, false}); }
+  void out(const void* p, uint64_t bytes) { if (bytes) all.push_back({(uintptr_t)p, (uintptr_t)p + bytes, true}); }
+  bool clash() {
+    std::sort(all.begin(), all.end(), [](const Span& x, const Span& y) { return x.lo < y.lo; });
+    uintptr_t in_end = 0, out_end = 0;
+    for (const Span& s : all) {
+      if (s.lo < out_end || (s.out && s.lo < in_end)) return true;
+      uintptr_t& end = s.out ? out_end : in_end;
+      end = std::max(end, s.hi);
+    }
+    return false;
+  }
+};
+
+constexpr uint64_t kMaxTokens = (uint64_t)1 << 20, kMaxDim = (uint64_t)1 << 16, kMaxVocab = (uint64_t)1 << 24;
+constexpr uint64_t kMaxLogits = (uint64_t)1 << 37, kMaxRouterTokens = (uint64_t)1 << 24;
+
+// The checks that size the workspace, and the shards they describe.
+int xent_sizes(int nranks, const size_t vocab[], size_t tokens, size_t dim, int dtype, XentArgs* a, Shards* all) {
+  if (!valid_ranks(nranks) || !vocab || !float_type(dtype)) return EMU_ERR_INVALID_ARGUMENT;
+  a->type = static_cast<DType>(dtype);
+  if (tokens > kMaxTokens || dim < 1 || dim > kMaxDim || dim * elem_size(a->type) % kVecBytes)
+    return EMU_ERR_INVALID_ARGUMENT;
+  uint64_t total = 0;
+  for (int r = 0; r < nranks; ++r) {
+    if (vocab[r] > kMaxVocab) return EMU_ERR_INVALID_ARGUMENT;
+    all->rows[r] = (uint32_t)vocab[r];
+    all->id0[r] = (uint32_t)total;
+    total += vocab[r];
+  }
+  if (total < 1 || total > kMaxVocab || tokens * total > kMaxLogits) return EMU_ERR_INVALID_ARGUMENT;
+  all->nranks = (uint32_t)nranks;
+  a->tokens = (uint32_t)tokens;
+  a->dim = (uint32_t)dim;
+  return EMU_SUCCESS;
+}
+
+int xent_call(int nranks, const void* x, const void* const w[], const size_t vocab[], const long long* targets,
+              size_t tokens, size_t dim, float* loss, float* lse, const float* dloss, void* dx, void* const dw[],
+              int dtype, void* workspace, size_t workspace_bytes, void* stream, bool grad) {
+  XentArgs a{};
+  Shards all{};
+  if (int e = xent_sizes(nranks, vocab, tokens, dim, dtype, &a, &all)) return e;
+  if (!w || (grad && !dx && !dw)) return EMU_ERR_INVALID_ARGUMENT;
+  const uint64_t row = (uint64_t)dim * elem_size(a.type);
+  Spans spans;
+  for (int r = 0; r < nranks; ++r) {
+    if (!vocab[r]) continue;
+    if (!usable(w[r]) || (dw && !usable(dw[r]))) return EMU_ERR_INVALID_ARGUMENT;
+    all.w[r] = w[r];
+    all.dw[r] = dw ? dw[r] : nullptr;
+    spans.in(w[r], vocab[r] * row);
+    if (dw) spans.out(dw[r], vocab[r] * row);
+  }
+  if (tokens == 0) {
+    if (spans.clash()) return EMU_ERR_INVALID_ARGUMENT;
+    a.cus = current_cus();
+    if (!dw) return EMU_SUCCESS;
+    return xent_clear(a, all, stream) == hipSuccess ? EMU_SUCCESS : EMU_ERR_HIP;
+  }
+  if (!usable(x) || !usable(targets) || !usable(lse) || !usable(workspace)) return EMU_ERR_INVALID_ARGUMENT;
+  if (grad ? !usable(dloss) || (dx && !usable(dx)) : !usable(loss)) return EMU_ERR_INVALID_ARGUMENT;
+  a.x = x;
+  a.targets = reinterpret_cast<const int64_t*>(targets);
+  a.loss = loss;
+  a.lse = lse;
+  a.dloss = dloss;
+  a.dx = dx;
+  a.cus = current_cus();
+  const size_t need = grad ? xent_grad_space(a, all, dx != nullptr, dw != nullptr).bytes : xent_loss_space(a, all).bytes;
+  if (workspace_bytes < need) return EMU_ERR_INVALID_ARGUMENT;
+  spans.in(x, tokens * row);
+  spans.in(targets, tokens * sizeof(int64_t));
+  if (grad) {
+    spans.in(lse, tokens * sizeof(float));
+    spans.in(dloss, tokens * sizeof(float));
+    if (dx) spans.out(dx, tokens * row);
+  } else {
+    spans.out(loss, tokens * sizeof(float));
+    spans.out(lse, tokens * sizeof(float));
+  }
+  spans.out(workspace, need);
+  if (spans.clash()) return EMU_ERR_INVALID_ARGUMENT;
+  char* ws = static_cast<char*>(workspace);
+  return (grad ? xent_grad(a, all, ws, stream) : xent_loss(a, all, ws, stream)) == hipSuccess ? EMU_SUCCESS
+                                                                                            : EMU_ERR_HIP;
+}
+
+int balance_sizes(int nranks, const size_t tokens[], size_t nexperts, BalanceArgs* a) {
+  if (!valid_ranks(nranks) || !tokens || nexperts < 1 || nexperts > EMU_MAX_EXPERTS) return EMU_ERR_INVALID_ARGUMENT;
+  for (int r = 0; r < nranks; ++r) {
+    if (tokens[r] > kMaxRouterTokens) return EMU_ERR_INVALID_ARGUMENT;
+    a->tokens[r] = (uint32_t)tokens[r];
+  }
+  a->nranks = (uint32_t)nranks;
+  a->nexperts = (uint32_t)nexperts;
+  a->cus = current_cus();
+  return EMU_SUCCESS;
+}
+
+int ortho_sizes(int nranks, size_t rows, size_t cols, int dtype, OrthoArgs* a) {
+  if (!valid_ranks(nranks) || !float_type(dtype)) return EMU_ERR_INVALID_ARGUMENT;
+  if (rows > ((size_t)1 << 20) || cols > ((size_t)1 << 20) || rows * cols > ((size_t)1 << 32))
+    return EMU_ERR_INVALID_ARGUMENT;
+  a->nranks = (uint32_t)nranks;
+  a->rows = (uint32_t)rows;
+  a->cols = (uint32_t)cols;
+  a->type = static_cast<DType>(dtype);
+  return EMU_SUCCESS;
+}
+
+}  // namespace
+}  // namespace emu
+
+using namespace emu;
+
+extern "C" {
+
+int emu_cross_entropy_workspace(int nranks, const size_t vocab[], size_t tokens, size_t dim, int dtype, int want_dx,
+                                int want_dw, size_t* bytes) {
+  if (!bytes) return EMU_ERR_INVALID_ARGUMENT;
+  XentArgs a{};
+  Shards all{};
+  if (int e = xent_sizes(nranks, vocab, tokens, dim, dtype, &a, &all)) return e;
+  *bytes = 0;
+  if (tokens == 0) return EMU_SUCCESS;
+  a.cus = current_cus();
+  *bytes = want_dx || want_dw ? xent_grad_space(a, all, want_dx != 0, want_dw != 0).bytes : xent_loss_space(a, all).bytes;
+  return EMU_SUCCESS;
+}
+
+int emu_cross_entropy(int nranks, const void* x, const void* const w[], const size_t vocab[],
+                      const long long* targets, size_t tokens, size_t dim, float* loss, float* lse, int dtype,
+                      void* workspace, size_t workspace_bytes, void* stream) {
+  return xent_call(nranks, x, w, vocab, targets, tokens, dim, loss, lse, nullptr, nullptr, nullptr, dtype, workspace,
+                   workspace_bytes, stream, false);
+}
+
+int emu_cross_entropy_grad(int nranks, const void* x, const void* const w[], const size_t vocab[],
+                           const long long* targets, const float* lse, const float* dloss, size_t tokens, size_t dim,
+                           void* dx, void* const dw[], int dtype, void* workspace, size_t workspace_bytes,
+                           void* stream) {
+  return xent_call(nranks, x, w, vocab, targets, tokens, dim, nullptr, const_cast<float*>(lse), dloss, dx, dw, dtype,
+                   workspace, workspace_bytes, stream, true);
+}
+
+int emu_balance_loss_workspace(int nranks, const size_t tokens[], size_t nexperts, size_t* bytes) {
+  if (!bytes) return EMU_ERR_INVALID_ARGUMENT;
+  BalanceArgs a{};
+  if (int e = balance_sizes(nranks, tokens, nexperts, &a)) return e;
+  *bytes = balance_space(a);
+  return EMU_SUCCESS;
+}
+
+int emu_balance_loss(int nranks, const void* const logits[], const int* const experts[], const size_t tokens[],
+                     size_t nexperts, size_t topk, float coef, long long* counts, float* loss,
+                     void* const dlogits[], int dtype, void* workspace, size_t workspace_bytes, void* stream) {
+  BalanceArgs a{};
+  if (!float_type(dtype) || !logits || !experts || topk < 1 || topk > nexperts || !std::isfinite(coef))
+    return EMU_ERR_INVALID_ARGUMENT;
+  if (!usable(counts) || !usable(loss) || !usable(workspace)) return EMU_ERR_INVALID_ARGUMENT;
+  if (int e = balance_sizes(nranks, tokens, nexperts, &a)) return e;
+  a.type = static_cast<DType>(dtype);
+  a.topk = (uint32_t)topk;
+  a.coef = coef;
+  a.grad = dlogits != nullptr;
+  a.counts = reinterpret_cast<int64_t*>(counts);
+  a.loss = loss;
+  const uint64_t row = (uint64_t)nexperts * elem_size(a.type);
+  const size_t need = balance_space(a);
+  if (workspace_bytes < need) return EMU_ERR_INVALID_ARGUMENT;
+  Spans spans;
+  for (int r = 0; r < nranks; ++r) {
+    if (!tokens[r]) continue;
+    if (!usable(logits[r]) || !usable(experts[r]) || (dlogits && !usable(dlogits[r]))) return EMU_ERR_INVALID_ARGUMENT;
+    a.logits[r] = logits[r];
+    a.experts[r] = experts[r];
+    a.dlogits[r] = dlogits ? dlogits[r] : nullptr;
+    spans.in(logits[r], tokens[r] * row);
+    spans.in(experts[r], tokens[r] * topk * sizeof(int32_t));
+    if (dlogits) spans.out(dlogits[r], tokens[r] * row);
+  }
+  spans.out(counts, (nranks + 1) * nexperts * sizeof(int64_t));
+  spans.out(loss, sizeof(float));
+  spans.out(workspace, need);
+  if (spans.clash()) return EMU_ERR_INVALID_ARGUMENT;
+  return balance_loss(a, static_cast<char*>(workspace), stream) == hipSuccess ? EMU_SUCCESS : EMU_ERR_HIP;
+}
+
+int emu_orthogonalize_workspace(int nranks, size_t rows, size_t cols, int dtype, size_t* bytes) {
+  if (!bytes) return EMU_ERR_INVALID_ARGUMENT;
+  OrthoArgs a{};
+  if (int e = ortho_sizes(nranks, rows, cols, dtype, &a)) return e;
+  *bytes = rows && cols ? ortho_space(a) : 0;
+  return EMU_SUCCESS;
+}
+
+int emu_orthogonalize(int nranks, const void* const sendbufs[], void* const recvbufs[], size_t rows, size_t cols,
+                      int steps, const float* coeffs, int dtype, void* workspace, size_t workspace_bytes,
+                      void* stream) {
+  static const float kDefault[3] = {3.4445f, -4.7750f, 2.0315f};
+  OrthoArgs a{};
+  if (int e = ortho_sizes(nranks, rows, cols, dtype, &a)) return e;
+  if (!sendbufs || !recvbufs || steps < 1 || steps > kMaxOrthoSteps) return EMU_ERR_INVALID_ARGUMENT;
+  for (int i = 0; i < 3 * steps; ++i) {
+    a.coeffs[i] = coeffs ? coeffs[i] : kDefault[i % 3];
+    if (!std::isfinite(a.coeffs[i])) return EMU_ERR_INVALID_ARGUMENT;
+  }
+  a.steps = steps;
+  const uint64_t bytes = (uint64_t)rows * cols * elem_size(a.type);
+  if (bytes == 0) return EMU_SUCCESS;
+  for (int r = 0; r < nranks; ++r)
+    if (!usable(sendbufs[r]) || !usable(recvbufs[r])) return EMU_ERR_INVALID_ARGUMENT;
+  if (!usable(workspace)) return EMU_ERR_INVALID_ARGUMENT;
+  const size_t need = ortho_space(a);
+  if (workspace_bytes < need) return EMU_ERR_INVALID_ARGUMENT;
+  Spans spans;
+  for (int r = 0; r < nranks; ++r) {
+    a.in[r] = sendbufs[r];
+    a.out[r] = recvbufs[r];
+    if (sendbufs[r] != recvbufs[r]) spans.in(sendbufs[r], bytes);
+    spans.out(recvbufs[r], bytes);
+  }
+  spans.out(workspace, need);
+  if (spans.clash()) return EMU_ERR_INVALID_ARGUMENT;
+  a.cus = current_cus();
+  return orthogonalize(a, static_cast<char*>(workspace), stream) == hipSuccess ? EMU_SUCCESS : EMU_ERR_HIP;
+}
+
+}  // extern "C"

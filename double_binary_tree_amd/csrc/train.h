@@ -1,0 +1,103 @@
+// The operators of a sharded training step: what the entry points (train.cpp)
+// hand to the kernels.  Plain structs, no HIP types.
+#pragma once
+
+#include <cstddef>
+#include <cstdint>
+
+#include "common.h"
+
+namespace emu {
+
+// --- cross entropy (xent.hip) ------------------------------------------------
+
+// A run of vocabulary rows of each rank, packed: rank r's rows [row0, row0 +
+// rows) sit at positions first .. first + rows - 1.  Positions of a rank
+// start at multiples of kShardAlign, so every vector of a packed row is
+// whole and belongs to one rank.
+constexpr uint32_t kShardAlign = 8;
+struct Shards {
+  const void* w[kMaxRanks];
+  void* dw[kMaxRanks];
+  uint32_t row0[kMaxRanks];
+  uint32_t rows[kMaxRanks];
+  uint32_t first[kMaxRanks];
+  uint32_t id0[kMaxRanks];      // vocabulary index of the rank's first row in the run
+  uint32_t nranks;
+  uint32_t width;               // positions in all
+};
+
+struct XentArgs {
+  const void* x;
+  const int64_t* targets;
+  float* loss;
+  float* lse;                   // output of the loss, input of the gradient
+  const float* dloss;
+  void* dx;
+  uint32_t tokens, dim;
+  DType type;
+  int cus;
+};
+
+// Device memory of one call, carved from the caller's workspace.
+struct XentLossSpace {
+  size_t stats = 0;             // [vocabulary tiles][tokens] running (max, sum)
+  size_t label = 0;             // [tokens] the target's logit
+  size_t bytes = 0;
+};
+struct XentGradSpace {
+  size_t scale = 0;             // factor on the stored gradients, and its inverse
+  size_t xt = 0;                // x transposed [dim][tpitch]
+  size_t wt = 0;                // the run's rows transposed [dim][vpitch]
+  size_t g = 0, gt = 0;         // d loss / d logits of the run [tokens][vpitch] and transposed [width][tpitch]
+  size_t part = 0;              // [splits][tokens][dim] f32 parts of dx
+  size_t bytes = 0;
+  uint32_t tpitch = 0, vpitch = 0;   // in elements
+  uint32_t width = 0;           // positions per run, at most
+  uint32_t splits = 1;
+};
+
+XentLossSpace xent_loss_space(const XentArgs& a, const Shards& all);
+XentGradSpace xent_grad_space(const XentArgs& a, const Shards& all, bool dx, bool dw);
+// These return a hipError_t as int.  xent_clear: the gradient of no tokens,
+// zeros in every dw.
+int xent_clear(const XentArgs& a, const Shards& all, void* stream);
+int xent_loss(const XentArgs& a, const Shards& all, char* workspace, void* stream);
+int xent_grad(const XentArgs& a, const Shards& all, char* workspace, void* stream);
+
+// --- router balance loss (balance.hip) ---------------------------------------
+
+struct BalanceArgs {
+  const void* logits[kMaxRanks];
+  const int32_t* experts[kMaxRanks];
+  void* dlogits[kMaxRanks];
+  uint32_t tokens[kMaxRanks];
+  uint32_t nranks, nexperts, topk;
+  float coef;
+  bool grad;                    // dlogits are wanted
+  int64_t* counts;              // [nranks + 1][nexperts]
+  float* loss;
+  DType type;
+  int cus;
+};
+size_t balance_space(const BalanceArgs& a);
+int balance_loss(const BalanceArgs& a, char* workspace, void* stream);
+
+// --- orthogonalisation (ortho.hip) -------------------------------------------
+
+constexpr int kMaxOrthoSteps = 16;
+struct OrthoArgs {
+  const void* in[kMaxRanks];
+  void* out[kMaxRanks];
+  uint32_t nranks, rows, cols;
+  int steps;
+  float coeffs[3 * kMaxOrthoSteps];
+  DType type;
+  int cus;
+};
+size_t ortho_space(const OrthoArgs& a);
+int orthogonalize(const OrthoArgs& a, char* workspace, void* stream);
+
+inline size_t align_up(size_t x, size_t a) { return (x + a - 1) / a * a; }
+
+}  // namespace emu

@@ -1,0 +1,638 @@
+// Softmax cross entropy of hidden states x [tokens][dim] against vocabulary
+// rows split over the ranks, w_r [vocab_r][dim], without keeping the logits:
+//   z_tv = x_t . w_v,  lse_t = log sum_v exp z_tv,  loss_t = lse_t - z_t,y(t),
+//   g_tv = dloss_t (exp(z_tv - lse_t) - [v = y(t)]),
+//   dx = g w,  dw = g^T x.
+//
+// The loss is one product whose epilogue keeps, per tile and token, the
+// largest logit m and sum exp(z - m) over the tile's rows; xent_join adds
+// the tiles in vocabulary (so rank) order:
+// (m, s) + (m', s') = (M, s exp(m - M) + s' exp(m' - M)), M = max(m, m').
+//
+// The gradient takes the vocabulary in runs: the product is formed again, its
+// epilogue writes g of the run in the inputs' type (token-major and
+// transposed), and two more products read it.  dx is summed in f32 over the
+// runs and rounded once.
+//
+// Vocabulary rows are the product's first operand (lanes hold 4 consecutive
+// rows of one token), so a token's maximum and sum are mostly within a lane.
+#include "tile.h"
+#include "train.h"
+
+namespace emu {
+
+namespace {
+
+template <DType T>
+struct Elem;
+template <>
+struct Elem<DType::F32> { typedef float type; };
+template <>
+struct Elem<DType::F16> { typedef _Float16 type; };
+template <>
+struct Elem<DType::BF16> { typedef __bf16 type; };
+
+constexpr float kLog2e = 1.44269504088896341f;
+__device__ __forceinline__ float exp_of(float x) { return __builtin_amdgcn_exp2f(x * kLog2e); }
+
+// The rank whose tile rows (of `bm` vocabulary rows each) include `m`; m
+// becomes the tile within the rank.
+__device__ __forceinline__ uint32_t rank_of_tile(const Shards& s, uint32_t bm, uint32_t& m) {
+  uint32_t r = 0;
+  for (; r + 1 < s.nranks; ++r) {
+    const uint32_t n = (s.rows[r] + bm - 1) / bm;
+    if (m < n) break;
+    m -= n;
+  }
+  return r;
+}
+uint32_t tiles_of(const Shards& s, uint32_t bm) {
+  uint32_t n = 0;
+  for (uint32_t r = 0; r < s.nranks; ++r) n += (s.rows[r] + bm - 1) / bm;
+  return n;
+}
+
+// exp(m - M) with the empty tile's m = -inf giving 0.
+__device__ __forceinline__ void merge(float& m, float& s, float m2, float s2) {
+  const float big = fmaxf(m, m2), ref = big == -INFINITY ? 0.0f : big;
+  s = s * exp_of(m - ref) + s2 * exp_of(m2 - ref);
+  m = big;
+}
+
+struct LossTile {
+  const void* x;
+  const int64_t* targets;
+  float2* stats;
+  float* label;
+  uint32_t tokens, dim, tm, tn, band;
+};
+
+template <DType T, class K>
+__global__ __launch_bounds__(K::threads) void xent_stats(Shards sh, LossTile p) {
+  __shared__ __attribute__((aligned(16))) char lds[K::lds_bytes];
+  constexpr int ES = sizeof(typename Elem<T>::type);
+  uint32_t m, n;
+  tile_of(blockIdx.x, p.tm, p.tn, p.band, m, n);
+  const uint32_t tile = m, r = rank_of_tile(sh, K::BM, m);
+  const uint32_t ld = p.dim * ES, row = m * K::BM, tok = n * K::BN;
+  const int rows = (int)(sh.rows[r] - row);
+  const Operand a{static_cast<const char*>(sh.w[r]) + (uint64_t)(sh.row0[r] + row) * ld, ld, rows};
+  const Operand b{static_cast<const char*>(p.x) + (uint64_t)tok * ld, ld, (int)(p.tokens - tok)};
+  typename K::Acc acc = {};
+  K::run(a, b, ld, lds_address(lds), acc);
+
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, wm = wave / K::WGN, wn = wave % K::WGN;
+  __syncthreads();
+  float2* part = reinterpret_cast<float2*>(lds);          // [WGM][BN]
+#pragma unroll
+  for (int j = 0; j < K::NF; ++j) {
+    const uint32_t c = wn * K::WN + j * 16 + (lane & 15);
+    // the target's row within this tile, if it is here
+    int y = -1;
+    if (tok + c < p.tokens) {
+      const int64_t at = p.targets[tok + c] - (int64_t)sh.id0[r] - row;
+      if (at >= 0 && at < rows) y = (int)at;
+    }
+    float big = -INFINITY;
+#pragma unroll
+    for (int i = 0; i < K::MF; ++i)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const int v = wm * K::WM + i * 16 + 4 * (lane >> 4) + e;
+        if (v >= rows) acc[i][j][e] = -INFINITY;
+        else if (v == y) p.label[tok + c] = acc[i][j][e];
+        big = fmaxf(big, acc[i][j][e]);
+      }
+    big = fmaxf(big, __shfl_xor(big, 16));
+    big = fmaxf(big, __shfl_xor(big, 32));
+    const float ref = big == -INFINITY ? 0.0f : big;
+    float s = 0.0f;
+#pragma unroll
+    for (int i = 0; i < K::MF; ++i)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) s += exp_of(acc[i][j][e] - ref);
+    s += __shfl_xor(s, 16);
+    s += __shfl_xor(s, 32);
+    if (lane < 16) part[wm * K::BN + c] = make_float2(big, s);
+  }
+  __syncthreads();
+  for (uint32_t c = threadIdx.x; c < K::BN; c += K::threads) {
+    if (tok + c >= p.tokens) break;
+    float2 q = part[c];
+#pragma unroll
+    for (int w = 1; w < K::WGM; ++w) merge(q.x, q.y, part[w * K::BN + c].x, part[w * K::BN + c].y);
+    p.stats[(uint64_t)tile * p.tokens + tok + c] = q;
+  }
+}
+
+// 16 tokens a workgroup, 16 lanes each: lane k merges a contiguous share of
+// the tiles, and the 16 shares are merged in order.
+constexpr int kJoin = 16;
+__global__ __launch_bounds__(kJoin* kJoin) void xent_join(const float2* __restrict__ stats, const float* __restrict__ label,
+                                                         const int64_t* __restrict__ targets, uint32_t tokens,
+                                                         uint32_t tiles, int64_t vocab, float* __restrict__ loss,
+                                                         float* __restrict__ lse) {
+  __shared__ float2 part[kJoin][kJoin];
+  const uint32_t c = threadIdx.x % kJoin, k = threadIdx.x / kJoin, t = blockIdx.x * kJoin + c;
+  const uint32_t share = (tiles + kJoin - 1) / kJoin;
+  float m = -INFINITY, s = 0.0f;
+  if (t < tokens)
+    for (uint32_t i = k * share; i < min((k + 1) * share, tiles); ++i) {
+      const float2 q = stats[(uint64_t)i * tokens + t];
+      merge(m, s, q.x, q.y);
+    }
+  part[k][c] = make_float2(m, s);
+  __syncthreads();
+  if (k == 0 && t < tokens) {
+    for (int i = 1; i < kJoin; ++i) merge(m, s, part[i][c].x, part[i][c].y);
+    const float l = m + logf(s);
+    const int64_t y = targets[t];
+    lse[t] = l;
+    loss[t] = y >= 0 && y < vocab ? l - label[t] : 0.0f;
+  }
+}
+
+// f16 gradients are stored scaled by the power of two that brings the largest
+// |dloss| to [2^14, 2^15): |exp(z - lse) - 1| is at most 1 (for an lse of
+// these logits), and a probability of 2^-29 still keeps every bit.
+__global__ __launch_bounds__(1024) void xent_scale(const float* __restrict__ dloss, const int64_t* __restrict__ targets,
+                                                   uint32_t tokens, int64_t vocab, float* __restrict__ scale) {
+  __shared__ float part[16];
+  float big = 0.0f;
+  for (uint32_t t = threadIdx.x; t < tokens; t += 1024) {
+    const int64_t y = targets[t];
+    const float d = fabsf(dloss[t]);
+    if (y >= 0 && y < vocab && d < INFINITY) big = fmaxf(big, d);
+  }
+  for (int d = 1; d < 64; d <<= 1) big = fmaxf(big, __shfl_xor(big, d));
+  if ((threadIdx.x & 63) == 0) part[threadIdx.x >> 6] = big;
+  __syncthreads();
+  if (threadIdx.x == 0) {
+    for (int w = 1; w < 16; ++w) big = fmaxf(big, part[w]);
+    int e = 0;
+    (void)frexpf(big, &e);                                 // big = f 2^e, f in [1/2, 1)
+    e = big > 0.0f ? min(max(15 - e, -126), 126) : 0;
+    scale[0] = ldexpf(1.0f, e);
+    scale[1] = ldexpf(1.0f, -e);
+  }
+}
+
+// out[c][first + r] = in[r][c], r < rows, and zeros up to the next multiple of
+// kShardAlign; grid: x row tiles of every rank, y column tiles.  With
+// `targets`, rows without a target in [0, vocab) become zeros: a token without
+// a loss then adds nothing to dw, whatever its hidden state holds.
+template <class E>
+__global__ __launch_bounds__(256) void transpose_rows(Shards sh, E* __restrict__ out, uint32_t dim, uint32_t pitch,
+                                                      const int64_t* __restrict__ targets, int64_t vocab) {
+  constexpr int B = 64;
+  __shared__ E tile[B][B + 4 / sizeof(E)];
+  uint32_t m = blockIdx.x;
+  const uint32_t r = rank_of_tile(sh, B, m);
+  const E* in = static_cast<const E*>(sh.w[r]) + (uint64_t)sh.row0[r] * dim;
+  const uint32_t rows = sh.rows[r], pad = (rows + kShardAlign - 1) / kShardAlign * kShardAlign;
+  const uint32_t r0 = m * B, c0 = blockIdx.y * B, x = threadIdx.x % B, y = threadIdx.x / B;
+  for (uint32_t i = y; i < B; i += 4) {
+    bool take = r0 + i < rows && c0 + x < dim;
+    if (take && targets) take = targets[r0 + i] >= 0 && targets[r0 + i] < vocab;
+    tile[i][x] = take ? in[(uint64_t)(r0 + i) * dim + c0 + x] : (E)0.0f;
+  }
+  __syncthreads();
+  for (uint32_t i = y; i < B; i += 4)
+    if (c0 + i < dim && r0 + x < pad) out[(uint64_t)(c0 + i) * pitch + sh.first[r] + r0 + x] = tile[x][i];
+}
+
+struct GradTile {
+  const void* x;
+  const int64_t* targets;
+  const float* lse;
+  const float* dloss;
+  const float* scale;          // null: 1
+  void* g;
+  void* gt;                    // null: not wanted
+  uint32_t tokens, dim, vpitch, tpitch, tm, tn, band;
+  int64_t vocab;
+};
+
+// g of the run's rows for every token.  Positions between a rank's last row
+// and the next multiple of kShardAlign, and transposed columns past the last
+// token, become zeros: the products that read g go over whole vectors.
+template <DType T, class K>
+__global__ __launch_bounds__(K::threads) void xent_dlogits(Shards sh, GradTile p) {
+  __shared__ __attribute__((aligned(16))) char lds[K::lds_bytes];
+  typedef typename Elem<T>::type E;
+  typedef E E4 __attribute__((ext_vector_type(4)));
+  constexpr int ES = sizeof(E);
+  uint32_t m, n;
+  tile_of(blockIdx.x, p.tm, p.tn, p.band, m, n);
+  const uint32_t r = rank_of_tile(sh, K::BM, m);
+  const uint32_t ld = p.dim * ES, row = m * K::BM, tok = n * K::BN;
+  const int rows = (int)(sh.rows[r] - row);
+  const int padded = (int)((sh.rows[r] + kShardAlign - 1) / kShardAlign * kShardAlign - row);
+  const Operand a{static_cast<const char*>(sh.w[r]) + (uint64_t)(sh.row0[r] + row) * ld, ld, rows};
+  const Operand b{static_cast<const char*>(p.x) + (uint64_t)tok * ld, ld, (int)(p.tokens - tok)};
+  typename K::Acc acc = {};
+  K::run(a, b, ld, lds_address(lds), acc);
+
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, wm = wave / K::WGN, wn = wave % K::WGN;
+  const float scale = p.scale ? p.scale[0] : 1.0f;
+  const uint32_t first = sh.first[r] + row;
+  E* g = static_cast<E*>(p.g);
+  E* gt = static_cast<E*>(p.gt);
+#pragma unroll
+  for (int j = 0; j < K::NF; ++j) {
+    const uint32_t t = tok + wn * K::WN + j * 16 + (lane & 15), tt = min(t, p.tokens - 1);
+    const int64_t id = p.targets[tt];
+    const bool counted = id >= 0 && id < p.vocab && t < p.tokens;
+    const int64_t at = id - (int64_t)sh.id0[r] - row;
+    const int y = at >= 0 && at < rows ? (int)at : -1;
+    const float lse = p.lse[tt], d = p.dloss[tt] * scale;
+#pragma unroll
+    for (int i = 0; i < K::MF; ++i) {
+      const int v = wm * K::WM + i * 16 + 4 * (lane >> 4);
+      E4 out;
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const float q = exp_of(acc[i][j][e] - lse) - (v + e == y ? 1.0f : 0.0f);
+        out[e] = (E)(counted && v + e < rows ? d * q : 0.0f);
+      }
+      if (v >= padded) continue;
+      if (g && t < p.tokens) *reinterpret_cast<E4*>(g + (uint64_t)t * p.vpitch + first + v) = out;
+      if (gt && t < p.tpitch) {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) gt[(uint64_t)(first + v + e) * p.tpitch + t] = out[e];
+      }
+    }
+  }
+}
+
+// dx: first operand the run's rows transposed [dim][width], second g
+// [tokens][width]; workgroup z of gridDim.y sums a share of the width into
+// part[z].
+struct DxTile {
+  const void* wt;
+  const void* g;
+  float* part;
+  uint32_t tokens, dim, width, vpitch, share, tm, tn, band;
+  bool add;
+};
+template <DType T, class K>
+__global__ __launch_bounds__(K::threads) void xent_dx(DxTile p) {
+  __shared__ __attribute__((aligned(16))) char lds[K::lds_bytes];
+  constexpr int ES = sizeof(typename Elem<T>::type);
+  uint32_t m, n;
+  tile_of(blockIdx.x, p.tm, p.tn, p.band, m, n);
+  const uint32_t k0 = blockIdx.y * p.share, k1 = min(k0 + p.share, p.width);
+  const uint32_t row = m * K::BM, tok = n * K::BN, ld = p.vpitch * ES;
+  typename K::Acc acc = {};
+  if (k0 < k1) {
+    const Operand a{static_cast<const char*>(p.wt) + (uint64_t)row * ld + (uint64_t)k0 * ES, ld, (int)(p.dim - row)};
+    const Operand b{static_cast<const char*>(p.g) + (uint64_t)tok * ld + (uint64_t)k0 * ES, ld, (int)(p.tokens - tok)};
+    K::run(a, b, (uint64_t)(k1 - k0) * ES, lds_address(lds), acc);
+  } else if (p.add) {
+    return;
+  }
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, wm = wave / K::WGN, wn = wave % K::WGN;
+  float* part = p.part + (uint64_t)blockIdx.y * p.tokens * p.dim;
+#pragma unroll
+  for (int j = 0; j < K::NF; ++j) {
+    const uint32_t t = tok + wn * K::WN + j * 16 + (lane & 15);
+#pragma unroll
+    for (int i = 0; i < K::MF; ++i) {
+      const uint32_t d = row + wm * K::WM + i * 16 + 4 * (lane >> 4);
+      if (t >= p.tokens || d >= p.dim) continue;
+      f32x4* at = reinterpret_cast<f32x4*>(part + (uint64_t)t * p.dim + d);
+      *at = p.add ? *at + acc[i][j] : acc[i][j];
+    }
+  }
+}
+
+// dx = (sum of the parts, in order) * unscale, rounded once; zeros for a token
+// without a loss.  Four values a lane (dim is a multiple of 4).
+template <DType T>
+__global__ __launch_bounds__(256) void xent_dx_join(const float* __restrict__ part, uint32_t splits, uint64_t quads,
+                                                    uint32_t per_token, const int64_t* __restrict__ targets,
+                                                    int64_t vocab, const float* __restrict__ scale,
+                                                    void* __restrict__ dx) {
+  typedef typename Elem<T>::type E;
+  typedef E E4 __attribute__((ext_vector_type(4)));
+  const float f = scale ? scale[1] : 1.0f;
+  for (uint64_t q = (uint64_t)blockIdx.x * 256 + threadIdx.x; q < quads; q += (uint64_t)gridDim.x * 256) {
+    f32x4 s = reinterpret_cast<const f32x4*>(part)[q];
+    for (uint32_t i = 1; i < splits; ++i) s += reinterpret_cast<const f32x4*>(part)[i * quads + q];
+    const int64_t y = targets[q / per_token];
+    const bool counted = y >= 0 && y < vocab;
+    E4 out;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) out[e] = (E)(counted ? s[e] * f : 0.0f);
+    reinterpret_cast<E4*>(dx)[q] = out;
+  }
+}
+
+// Zeros, 16 bytes a lane, for a rank's rows; grid: y ranks.
+__global__ __launch_bounds__(256) void xent_zero(Shards sh, uint64_t row_bytes) {
+  const uint64_t vecs = sh.rows[blockIdx.y] * row_bytes / kVecBytes;
+  for (uint64_t i = (uint64_t)blockIdx.x * 256 + threadIdx.x; i < vecs; i += (uint64_t)gridDim.x * 256)
+    static_cast<u32x4*>(sh.dw[blockIdx.y])[i] = u32x4{0, 0, 0, 0};
+}
+
+// dw: first operand x transposed [dim][tpitch], second g transposed
+// [width][tpitch].
+struct DwTile {
+  const void* xt;
+  const void* gt;
+  const float* scale;
+  uint32_t dim, tpitch, tm, tn, band;
+};
+template <DType T, class K>
+__global__ __launch_bounds__(K::threads) void xent_dw(Shards sh, DwTile p) {
+  __shared__ __attribute__((aligned(16))) char lds[K::lds_bytes];
+  typedef typename Elem<T>::type E;
+  typedef E E4 __attribute__((ext_vector_type(4)));
+  constexpr int ES = sizeof(E);
+  uint32_t m, n;
+  tile_of(blockIdx.x, p.tm, p.tn, p.band, m, n);
+  const uint32_t r = rank_of_tile(sh, K::BN, n), ld = p.tpitch * ES, col = m * K::BM, row = n * K::BN;
+  const Operand a{static_cast<const char*>(p.xt) + (uint64_t)col * ld, ld, (int)(p.dim - col)};
+  const Operand b{static_cast<const char*>(p.gt) + (uint64_t)(sh.first[r] + row) * ld, ld, (int)(sh.rows[r] - row)};
+  typename K::Acc acc = {};
+  K::run(a, b, ld, lds_address(lds), acc);
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, wm = wave / K::WGN, wn = wave % K::WGN;
+  const float f = p.scale ? p.scale[1] : 1.0f;
+  E* dw = static_cast<E*>(sh.dw[r]) + (uint64_t)sh.row0[r] * p.dim;
+#pragma unroll
+  for (int j = 0; j < K::NF; ++j) {
+    const uint32_t v = row + wn * K::WN + j * 16 + (lane & 15);
+#pragma unroll
+    for (int i = 0; i < K::MF; ++i) {
+      const uint32_t d = col + wm * K::WM + i * 16 + 4 * (lane >> 4);
+      if (v >= sh.rows[r] || d >= p.dim) continue;
+      E4 out;
+#pragma unroll
+      for (int e = 0; e < 4; ++e) out[e] = (E)(acc[i][j][e] * f);
+      *reinterpret_cast<E4*>(dw + (uint64_t)v * p.dim + d) = out;
+    }
+  }
+}
+
+// --- tile shapes -------------------------------------------------------------
+
+template <DType T>
+using Big = TileMma<T, 256, 256, 2, 4>;
+template <DType T>
+using Mid = TileMma<T, 128, 128, 2, 2>;
+template <DType T>
+using Thin = TileMma<T, 128, 64, 4, 1>;
+
+uint32_t ceil_div(uint32_t a, uint32_t b) { return (a + b - 1) / b; }
+
+// Large tiles once they fill every CU, else the small ones.
+enum Shape { kBig, kMid, kThin };
+Shape shape_of(uint64_t big_tiles, uint32_t second, int cus) {
+  if (big_tiles >= (uint64_t)cus) return kBig;
+  return second <= 64 ? kThin : kMid;
+}
+constexpr uint32_t kBmOf[] = {256, 128, 128};
+
+Shape loss_shape(const XentArgs& a, const Shards& s) {
+  return shape_of((uint64_t)tiles_of(s, 256) * ceil_div(a.tokens, 256), a.tokens, a.cus);
+}
+
+template <DType T, class K>
+hipError_t launch_stats(const XentArgs& a, const Shards& sh, float2* stats, float* label, uint32_t* tiles, hipStream_t s) {
+  LossTile p{a.x, a.targets, stats, label, a.tokens, a.dim, tiles_of(sh, K::BM), ceil_div(a.tokens, K::BN), 8};
+  *tiles = p.tm;
+  hipLaunchKernelGGL((xent_stats<T, K>), dim3(p.tm * p.tn), dim3(K::threads), 0, s, sh, p);
+  return hipGetLastError();
+}
+template <DType T>
+hipError_t loss_of(const XentArgs& a, const Shards& sh, char* ws, hipStream_t s) {
+  const XentLossSpace m = xent_loss_space(a, sh);
+  float2* stats = reinterpret_cast<float2*>(ws + m.stats);
+  float* label = reinterpret_cast<float*>(ws + m.label);
+  uint32_t tiles = 0;
+  hipError_t e;
+  switch (loss_shape(a, sh)) {
+    case kBig: e = launch_stats<T, Big<T>>(a, sh, stats, label, &tiles, s); break;
+    case kMid: e = launch_stats<T, Mid<T>>(a, sh, stats, label, &tiles, s); break;
+    default: e = launch_stats<T, Thin<T>>(a, sh, stats, label, &tiles, s); break;
+  }
+  if (e) return e;
+  int64_t vocab = 0;
+  for (uint32_t r = 0; r < sh.nranks; ++r) vocab += sh.rows[r];
+  hipLaunchKernelGGL(xent_join, dim3(ceil_div(a.tokens, kJoin)), dim3(kJoin * kJoin), 0, s, stats, label, a.targets,
+                     a.tokens, tiles, vocab, a.loss, a.lse);
+  return hipGetLastError();
+}
+
+// The next run of at most `width` positions after row `at` of the ranks'
+// rows laid end to end; advances `at`.
+Shards next_run(const Shards& all, uint32_t width, uint64_t& at) {
+  Shards s = all;
+  s.width = 0;
+  uint64_t begin = 0;
+  bool full = false;
+  const uint64_t from = at;
+  for (uint32_t r = 0; r < all.nranks; ++r) {
+    const uint64_t end = begin + all.rows[r];
+    s.first[r] = s.width;
+    s.rows[r] = 0;
+    s.row0[r] = 0;
+    if (end > from && !full) {
+      const uint64_t skip = from > begin ? from - begin : 0;
+      uint64_t n = std::min<uint64_t>(all.rows[r] - skip, width - s.width);
+      full = n < all.rows[r] - skip;
+      s.row0[r] = (uint32_t)skip;
+      s.rows[r] = (uint32_t)n;
+      s.id0[r] = (uint32_t)(begin + skip);
+      at += n;
+      s.width += (uint32_t)align_up(n, kShardAlign);
+      if (s.width >= width) full = true;
+    }
+    begin = end;
+  }
+  return s;
+}
+
+template <DType T, class K>
+hipError_t launch_dlogits(const XentArgs& a, const Shards& run, GradTile p, hipStream_t s) {
+  p.tm = tiles_of(run, K::BM);
+  p.tn = ceil_div(p.gt ? p.tpitch : p.tokens, K::BN);
+  p.band = 8;
+  hipLaunchKernelGGL((xent_dlogits<T, K>), dim3(p.tm * p.tn), dim3(K::threads), 0, s, run, p);
+  return hipGetLastError();
+}
+template <DType T, class K>
+hipError_t launch_dx(DxTile p, uint32_t splits, hipStream_t s) {
+  p.tm = ceil_div(p.dim, K::BM);
+  p.tn = ceil_div(p.tokens, K::BN);
+  p.band = 8;
+  hipLaunchKernelGGL((xent_dx<T, K>), dim3(p.tm * p.tn, splits), dim3(K::threads), 0, s, p);
+  return hipGetLastError();
+}
+template <DType T, class K>
+hipError_t launch_dw(const Shards& run, DwTile p, hipStream_t s) {
+  p.tm = ceil_div(p.dim, K::BM);
+  p.tn = tiles_of(run, K::BN);
+  p.band = 8;
+  hipLaunchKernelGGL((xent_dw<T, K>), dim3(p.tm * p.tn), dim3(K::threads), 0, s, run, p);
+  return hipGetLastError();
+}
+
+Shape dx_shape(const XentArgs& a, uint32_t splits) {
+  return shape_of((uint64_t)ceil_div(a.dim, 256) * ceil_div(a.tokens, 256) * splits, a.tokens, a.cus);
+}
+
+template <DType T>
+hipError_t grad_of(const XentArgs& a, const Shards& all, char* ws, hipStream_t s) {
+  typedef typename Elem<T>::type E;
+  const bool dx = a.dx != nullptr;
+  bool dw = false;
+  for (uint32_t r = 0; r < all.nranks; ++r) dw = dw || all.dw[r] != nullptr;
+  const XentGradSpace m = xent_grad_space(a, all, dx, dw);
+  const float* scale = nullptr;
+  int64_t vocab = 0;
+  for (uint32_t r = 0; r < all.nranks; ++r) vocab += all.rows[r];
+  hipError_t e;
+  if (T == DType::F16) {
+    hipLaunchKernelGGL(xent_scale, dim3(1), dim3(1024), 0, s, a.dloss, a.targets, a.tokens, vocab,
+                       reinterpret_cast<float*>(ws + m.scale));
+    scale = reinterpret_cast<const float*>(ws + m.scale);
+  }
+  if (dw) {
+    Shards xs{};
+    xs.w[0] = a.x;
+    xs.rows[0] = a.tokens;
+    xs.nranks = 1;
+    hipLaunchKernelGGL(transpose_rows<E>, dim3(ceil_div(a.tokens, 64), ceil_div(a.dim, 64)), dim3(256), 0, s, xs,
+                       reinterpret_cast<E*>(ws + m.xt), a.dim, m.tpitch, a.targets, vocab);
+  }
+  GradTile gp{};
+  gp.x = a.x;
+  gp.targets = a.targets;
+  gp.lse = a.lse;
+  gp.dloss = a.dloss;
+  gp.scale = scale;
+  gp.g = dx ? ws + m.g : nullptr;
+  gp.gt = dw ? ws + m.gt : nullptr;
+  gp.tokens = a.tokens;
+  gp.dim = a.dim;
+  gp.vpitch = m.vpitch;
+  gp.tpitch = m.tpitch;
+  gp.vocab = vocab;
+  uint64_t at = 0;
+  bool add = false;
+  while (at < (uint64_t)vocab) {
+    const Shards run = next_run(all, m.width, at);
+    switch (shape_of((uint64_t)tiles_of(run, 256) * ceil_div(a.tokens, 256), a.tokens, a.cus)) {
+      case kBig: e = launch_dlogits<T, Big<T>>(a, run, gp, s); break;
+      case kMid: e = launch_dlogits<T, Mid<T>>(a, run, gp, s); break;
+      default: e = launch_dlogits<T, Thin<T>>(a, run, gp, s); break;
+    }
+    if (e) return e;
+    if (dx) {
+      hipLaunchKernelGGL(transpose_rows<E>, dim3(tiles_of(run, 64), ceil_div(a.dim, 64)), dim3(256), 0, s, run,
+                         reinterpret_cast<E*>(ws + m.wt), a.dim, m.vpitch, nullptr, vocab);
+      DxTile p{};
+      p.wt = ws + m.wt;
+      p.g = ws + m.g;
+      p.part = reinterpret_cast<float*>(ws + m.part);
+      p.tokens = a.tokens;
+      p.dim = a.dim;
+      p.width = run.width;
+      p.vpitch = m.vpitch;
+      p.share = (uint32_t)align_up(ceil_div(run.width, m.splits), 64);
+      p.add = add;
+      add = true;
+      switch (dx_shape(a, m.splits)) {
+        case kBig: e = launch_dx<T, Big<T>>(p, m.splits, s); break;
+        case kMid: e = launch_dx<T, Mid<T>>(p, m.splits, s); break;
+        default: e = launch_dx<T, Thin<T>>(p, m.splits, s); break;
+      }
+      if (e) return e;
+    }
+    if (dw) {
+      DwTile p{};
+      p.xt = ws + m.xt;
+      p.gt = ws + m.gt;
+      p.scale = scale;
+      p.dim = a.dim;
+      p.tpitch = m.tpitch;
+      if ((uint64_t)ceil_div(a.dim, 256) * tiles_of(run, 256) >= (uint64_t)a.cus) e = launch_dw<T, Big<T>>(run, p, s);
+      else e = launch_dw<T, Mid<T>>(run, p, s);
+      if (e) return e;
+    }
+  }
+  if (dx) {
+    const uint64_t quads = (uint64_t)a.tokens * a.dim / 4;
+    hipLaunchKernelGGL(xent_dx_join<T>, dim3((uint32_t)std::min<uint64_t>((quads + 255) / 256, (uint64_t)a.cus * 16)),
+                       dim3(256), 0, s, reinterpret_cast<const float*>(ws + m.part), m.splits, quads,
+                       a.dim / 4, a.targets, vocab, scale, a.dx);
+  }
+  return hipGetLastError();
+}
+
+}  // namespace
+
+XentLossSpace xent_loss_space(const XentArgs& a, const Shards& all) {
+  XentLossSpace m;
+  const uint32_t tiles = tiles_of(all, kBmOf[loss_shape(a, all)]);
+  m.stats = 0;
+  m.label = align_up((size_t)tiles * a.tokens * sizeof(float2), 256);
+  m.bytes = m.label + align_up((size_t)a.tokens * sizeof(float), 256);
+  return m;
+}
+
+// A run takes as many positions as keep g (one of its two layouts) within
+// 2^27 values, at least 4096; dx is split over the width of a run until its
+// tiles reach two per CU, at most 64 ways.
+XentGradSpace xent_grad_space(const XentArgs& a, const Shards& all, bool dx, bool dw) {
+  XentGradSpace m;
+  const size_t es = (size_t)elem_size(a.type);
+  uint64_t positions = 0;
+  for (uint32_t r = 0; r < all.nranks; ++r) positions += align_up(all.rows[r], kShardAlign);
+  m.width = (uint32_t)std::min<uint64_t>(positions, std::max<uint64_t>(4096, (((uint64_t)1 << 27) / a.tokens) / 256 * 256));
+  m.vpitch = (uint32_t)align_up(m.width, 64);
+  m.tpitch = (uint32_t)align_up(a.tokens, kShardAlign);
+  const uint64_t tiles = (uint64_t)ceil_div(a.dim, 128) * ceil_div(a.tokens, 128);
+  while (m.splits < 64 && tiles * m.splits < 2 * (uint64_t)a.cus && m.width / (2 * m.splits) >= 256) m.splits *= 2;
+  size_t at = 0;
+  auto take = [&](size_t n) { const size_t p = at; at = align_up(at + n, 256); return p; };
+  m.scale = take(2 * sizeof(float));
+  if (dw) {
+    m.xt = take((size_t)a.dim * m.tpitch * es);
+    m.gt = take((size_t)m.width * m.tpitch * es);
+  }
+  if (dx) {
+    m.wt = take((size_t)a.dim * m.vpitch * es);
+    m.g = take((size_t)a.tokens * m.vpitch * es);
+    m.part = take((size_t)m.splits * a.tokens * a.dim * sizeof(float));
+  }
+  m.bytes = at;
+  return m;
+}
+
+int xent_clear(const XentArgs& a, const Shards& all, void* stream) {
+  hipLaunchKernelGGL(xent_zero, dim3(4 * a.cus, all.nranks), dim3(256), 0, static_cast<hipStream_t>(stream), all,
+                     (uint64_t)a.dim * elem_size(a.type));
+  return hipGetLastError();
+}
+
+int xent_loss(const XentArgs& a, const Shards& all, char* workspace, void* stream) {
+  hipStream_t s = static_cast<hipStream_t>(stream);
+  switch (a.type) {
+    case DType::F32: return loss_of<DType::F32>(a, all, workspace, s);
+    case DType::F16: return loss_of<DType::F16>(a, all, workspace, s);
+    default: return loss_of<DType::BF16>(a, all, workspace, s);
+  }
+}
+
+int xent_grad(const XentArgs& a, const Shards& all, char* workspace, void* stream) {
+  hipStream_t s = static_cast<hipStream_t>(stream);
+  switch (a.type) {
+    case DType::F32: return grad_of<DType::F32>(a, all, workspace, s);
+    case DType::F16: return grad_of<DType::F16>(a, all, workspace, s);
+    default: return grad_of<DType::BF16>(a, all, workspace, s);
+  }
+}
+
+}  // namespace emu

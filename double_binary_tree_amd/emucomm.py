@@ -88,6 +88,18 @@ def lib() -> ctypes.CDLL:
         L.emu_stream_probe.argtypes = [ctypes.c_int, ctypes.c_void_p, ctypes.c_void_p, ctypes.c_size_t,
                                        ctypes.c_void_p]
         L.emu_stream_probe.restype = ctypes.c_int
+        I, P, N = ctypes.c_int, ctypes.c_void_p, ctypes.c_size_t
+        PP, PN = ctypes.POINTER(ctypes.c_void_p), ctypes.POINTER(ctypes.c_size_t)
+        for name, types in (
+                ("emu_cross_entropy_workspace", [I, PN, N, N, I, I, I, PN]),
+                ("emu_cross_entropy", [I, P, PP, PN, P, N, N, P, P, I, P, N, P]),
+                ("emu_cross_entropy_grad", [I, P, PP, PN, P, P, P, N, N, P, PP, I, P, N, P]),
+                ("emu_balance_loss_workspace", [I, PN, N, PN]),
+                ("emu_balance_loss", [I, PP, PP, PN, N, N, ctypes.c_float, P, P, PP, I, P, N, P]),
+                ("emu_orthogonalize_workspace", [I, N, N, I, PN]),
+                ("emu_orthogonalize", [I, PP, PP, N, N, I, ctypes.POINTER(ctypes.c_float), I, P, N, P])):
+            getattr(L, name).argtypes = types
+            getattr(L, name).restype = I
         L.emu_strerror.argtypes = [ctypes.c_int]
         L.emu_strerror.restype = ctypes.c_char_p
         _lib = L
@@ -344,3 +356,277 @@ def all_gather_tensors(sends, recvs, stream=None) -> None:
     _check_tensors(recvs, sc * len(sends), dt)
     s = torch.cuda.current_stream() if stream is None else stream
     all_gather([t.data_ptr() for t in sends], [t.data_ptr() for t in recvs], sc, dt, s.cuda_stream)
+
+
+# --- operators of a sharded training step ------------------------------------
+#
+# The *_raw functions marshal pointers as integers and return the C code.  The
+# *_tensors functions check their tensors, run on the device that holds them
+# (whatever the current device is), on ``stream`` or that device's current
+# stream, and raise.  ``workspace`` is a CUDA uint8 tensor of at least the
+# size that the matching *_workspace function allocates; without one a call
+# allocates its own on that stream.  Calls that may overlap in time (two
+# streams, two captured graphs) need a workspace each.
+
+def _sizes(values):
+    return (ctypes.c_size_t * max(len(values), 1))(*[int(v) for v in values])
+
+
+def _opt_ptrs(ptrs):
+    return None if ptrs is None else _ptrs([0 if p is None else p for p in ptrs])
+
+
+def cross_entropy_workspace_raw(vocab, tokens: int, dim: int, dtype: int, want_dx: int, want_dw: int):
+    """(code, bytes) of emu_cross_entropy_workspace."""
+    n = ctypes.c_size_t(0)
+    e = lib().emu_cross_entropy_workspace(len(vocab), _sizes(vocab), tokens, dim, dtype, want_dx, want_dw,
+                                          ctypes.byref(n))
+    return e, int(n.value)
+
+
+def cross_entropy_raw(x, w, vocab, targets, tokens: int, dim: int, loss, lse, dtype: int, workspace,
+                      workspace_bytes: int, stream: int = 0) -> int:
+    return lib().emu_cross_entropy(len(vocab), x, _opt_ptrs(w), _sizes(vocab), targets, tokens, dim, loss, lse, dtype,
+                                   workspace, workspace_bytes, stream)
+
+
+def cross_entropy_grad_raw(x, w, vocab, targets, lse, dloss, tokens: int, dim: int, dx, dw, dtype: int, workspace,
+                           workspace_bytes: int, stream: int = 0) -> int:
+    return lib().emu_cross_entropy_grad(len(vocab), x, _opt_ptrs(w), _sizes(vocab), targets, lse, dloss, tokens, dim,
+                                        dx, _opt_ptrs(dw), dtype, workspace, workspace_bytes, stream)
+
+
+def balance_loss_workspace_raw(tokens, nexperts: int):
+    """(code, bytes) of emu_balance_loss_workspace."""
+    n = ctypes.c_size_t(0)
+    e = lib().emu_balance_loss_workspace(len(tokens), _sizes(tokens), nexperts, ctypes.byref(n))
+    return e, int(n.value)
+
+
+def balance_loss_raw(logits, experts, tokens, nexperts: int, topk: int, coef: float, counts, loss, dlogits, dtype: int,
+                     workspace, workspace_bytes: int, stream: int = 0) -> int:
+    return lib().emu_balance_loss(len(tokens), _opt_ptrs(logits), _opt_ptrs(experts), _sizes(tokens), nexperts, topk,
+                                  coef, counts, loss, _opt_ptrs(dlogits), dtype, workspace, workspace_bytes, stream)
+
+
+def orthogonalize_workspace_raw(nranks: int, rows: int, cols: int, dtype: int):
+    """(code, bytes) of emu_orthogonalize_workspace."""
+    n = ctypes.c_size_t(0)
+    e = lib().emu_orthogonalize_workspace(nranks, rows, cols, dtype, ctypes.byref(n))
+    return e, int(n.value)
+
+
+def orthogonalize_raw(sends, recvs, rows: int, cols: int, steps: int, coeffs, dtype: int, workspace,
+                      workspace_bytes: int, stream: int = 0) -> int:
+    c = None if coeffs is None else (ctypes.c_float * len(coeffs))(*coeffs)
+    return lib().emu_orthogonalize(len(sends), _opt_ptrs(sends), _opt_ptrs(recvs), rows, cols, steps, c, dtype,
+                                   workspace, workspace_bytes, stream)
+
+
+def _float_name(t) -> str:
+    import torch
+    names = {torch.float32: "f32", torch.float16: "f16", torch.bfloat16: "bf16"}
+    if t.dtype not in names:
+        raise ValueError("tensors must be float32, float16 or bfloat16")
+    return names[t.dtype]
+
+
+def _expect(t, shape, dtype, device, what: str):
+    if t.dtype != dtype or tuple(t.shape) != tuple(shape) or t.device != device or not t.is_contiguous():
+        raise ValueError(f"{what} must be a contiguous {dtype} tensor of shape {tuple(shape)} on {device}, got "
+                         f"{t.dtype} {tuple(t.shape)} on {t.device}")
+
+
+def _cuda_device(t):
+    if not t.is_cuda:
+        raise ValueError("tensors must be CUDA tensors")
+    return t.device
+
+
+def _allocate(code, nbytes: int, device, what: str):
+    import torch
+    _check(code, what)
+    return torch.empty(nbytes, dtype=torch.uint8, device=device)
+
+
+class _Launch:
+    """The device and stream of a call, and its workspace: the caller's, or
+    one that is allocated for this call on its stream."""
+
+    def __init__(self, device, stream, workspace, size, what: str):
+        import torch
+        self.guard = torch.cuda.device(device)
+        self.guard.__enter__()
+        try:
+            s = torch.cuda.current_stream(device) if stream is None else stream
+            if s.device != device:
+                raise ValueError(f"the stream is on {s.device}, the tensors on {device}")
+            self.stream = s.cuda_stream
+            if workspace is None:
+                code, n = size()
+                _check(code, what)
+                with torch.cuda.stream(s):
+                    workspace = torch.empty(n, dtype=torch.uint8, device=device)
+            elif workspace.device != device or workspace.dtype != torch.uint8 or not workspace.is_contiguous():
+                raise ValueError(f"the workspace must be a contiguous uint8 tensor on {device}")
+            self.tensor = workspace          # alive until the launches are enqueued
+            self.ptr, self.bytes = workspace.data_ptr(), workspace.numel()
+        except BaseException:
+            self.guard.__exit__(None, None, None)
+            raise
+
+    def __enter__(self):
+        return self
+
+    def __exit__(self, *exc):
+        return self.guard.__exit__(*exc)
+
+
+def _xent_shapes(x, ws):
+    device, name = _cuda_device(x), _float_name(x)
+    if x.dim() != 2 or not ws:
+        raise ValueError("x must be [tokens, dim], with one [vocab, dim] tensor per rank")
+    _expect(x, x.shape, x.dtype, device, "x")
+    for r, w in enumerate(ws):
+        _expect(w, (w.shape[0], x.shape[1]), x.dtype, device, f"w[{r}]")
+    return device, DTYPE[name], [w.shape[0] for w in ws], x.shape[0], x.shape[1]
+
+
+def cross_entropy_workspace(x, ws, grad: bool = False, want_dx: bool = True, want_dw: bool = True):
+    """A workspace for cross_entropy_tensors, or (``grad``) for
+    cross_entropy_grad_tensors, of tensors shaped like these."""
+    device, dt, vocab, tokens, dim = _xent_shapes(x, ws)
+    import torch
+    with torch.cuda.device(device):
+        e, n = cross_entropy_workspace_raw(vocab, tokens, dim, dt, int(grad and want_dx), int(grad and want_dw))
+        return _allocate(e, n, device, "emu_cross_entropy_workspace")
+
+
+def cross_entropy_tensors(x, ws, targets, loss, lse, workspace=None, stream=None) -> None:
+    """emu_cross_entropy: losses and log-sum-exps (f32 [tokens]) of hidden
+    states ``x`` [tokens, dim] against the ranks' vocabulary rows ``ws[r]``
+    [vocab_r, dim], for int64 ``targets`` [tokens] (outside the vocabulary: no
+    loss)."""
+    import torch
+    device, dt, vocab, tokens, dim = _xent_shapes(x, ws)
+    _expect(targets, (tokens,), torch.int64, device, "targets")
+    _expect(loss, (tokens,), torch.float32, device, "loss")
+    _expect(lse, (tokens,), torch.float32, device, "lse")
+    with _Launch(device, stream, workspace,
+                 lambda: cross_entropy_workspace_raw(vocab, tokens, dim, dt, 0, 0), "emu_cross_entropy_workspace") as c:
+        _check(cross_entropy_raw(x.data_ptr(), [w.data_ptr() for w in ws], vocab, targets.data_ptr(), tokens, dim,
+                                 loss.data_ptr(), lse.data_ptr(), dt, c.ptr, c.bytes, c.stream), "emu_cross_entropy")
+
+
+def cross_entropy_grad_tensors(x, ws, targets, lse, dloss, dx=None, dws=None, workspace=None, stream=None) -> None:
+    """emu_cross_entropy_grad: gradients of the hidden states into ``dx`` and
+    of every rank's rows into ``dws[r]`` (either may be None), for the f32
+    ``lse`` of the forward call and f32 ``dloss`` [tokens]."""
+    import torch
+    device, dt, vocab, tokens, dim = _xent_shapes(x, ws)
+    if dx is None and dws is None:
+        raise ValueError("need dx, dws or both")
+    _expect(targets, (tokens,), torch.int64, device, "targets")
+    _expect(lse, (tokens,), torch.float32, device, "lse")
+    _expect(dloss, (tokens,), torch.float32, device, "dloss")
+    if dx is not None:
+        _expect(dx, x.shape, x.dtype, device, "dx")
+    if dws is not None:
+        if len(dws) != len(ws):
+            raise ValueError("need one gradient tensor per rank")
+        for r, (w, d) in enumerate(zip(ws, dws)):
+            _expect(d, w.shape, w.dtype, device, f"dws[{r}]")
+    with _Launch(device, stream, workspace,
+                 lambda: cross_entropy_workspace_raw(vocab, tokens, dim, dt, int(dx is not None), int(dws is not None)),
+                 "emu_cross_entropy_workspace") as c:
+        _check(cross_entropy_grad_raw(x.data_ptr(), [w.data_ptr() for w in ws], vocab, targets.data_ptr(),
+                                      lse.data_ptr(), dloss.data_ptr(), tokens, dim,
+                                      None if dx is None else dx.data_ptr(),
+                                      None if dws is None else [d.data_ptr() for d in dws], dt, c.ptr, c.bytes,
+                                      c.stream), "emu_cross_entropy_grad")
+
+
+def _balance_shapes(logits):
+    if not logits or logits[0].dim() != 2:
+        raise ValueError("logits must hold one [tokens, experts] tensor per rank")
+    device, name = _cuda_device(logits[0]), _float_name(logits[0])
+    for r, z in enumerate(logits):
+        _expect(z, (z.shape[0], logits[0].shape[1]), logits[0].dtype, device, f"logits[{r}]")
+    return device, DTYPE[name], [z.shape[0] for z in logits], logits[0].shape[1]
+
+
+def balance_loss_workspace(logits):
+    """A workspace for balance_loss_tensors of logits shaped like these."""
+    import torch
+    device, _, tokens, nexperts = _balance_shapes(logits)
+    with torch.cuda.device(device):
+        e, n = balance_loss_workspace_raw(tokens, nexperts)
+        return _allocate(e, n, device, "emu_balance_loss_workspace")
+
+
+def balance_loss_tensors(logits, experts, coef: float, counts, loss, dlogits=None, workspace=None,
+                         stream=None) -> None:
+    """emu_balance_loss: per-rank router ``logits`` [tokens_r, experts] and
+    int32 ``experts`` [tokens_r, topk] (entries outside the range: dropped) to
+    int64 ``counts`` [ranks + 1, experts], the f32 ``loss`` [1] and, if given,
+    the logits' gradients ``dlogits``."""
+    import torch
+    device, dt, tokens, nexperts = _balance_shapes(logits)
+    if len(experts) != len(logits) or experts[0].dim() != 2:
+        raise ValueError("experts must hold one [tokens, topk] tensor per rank")
+    topk = experts[0].shape[1]
+    for r, z in enumerate(experts):
+        _expect(z, (tokens[r], topk), torch.int32, device, f"experts[{r}]")
+    _expect(counts, (len(logits) + 1, nexperts), torch.int64, device, "counts")
+    _expect(loss, (1,), torch.float32, device, "loss")
+    if dlogits is not None:
+        if len(dlogits) != len(logits):
+            raise ValueError("need one gradient tensor per rank")
+        for r, z in enumerate(dlogits):
+            _expect(z, logits[r].shape, logits[r].dtype, device, f"dlogits[{r}]")
+    with _Launch(device, stream, workspace, lambda: balance_loss_workspace_raw(tokens, nexperts),
+                 "emu_balance_loss_workspace") as c:
+        _check(balance_loss_raw([z.data_ptr() for z in logits], [z.data_ptr() for z in experts], tokens, nexperts,
+                                topk, coef, counts.data_ptr(), loss.data_ptr(),
+                                None if dlogits is None else [z.data_ptr() for z in dlogits], dt, c.ptr, c.bytes,
+                                c.stream), "emu_balance_loss")
+
+
+def _ortho_shapes(sends):
+    if not sends or sends[0].dim() != 2:
+        raise ValueError("need one [rows, cols] matrix per rank")
+    device, name = _cuda_device(sends[0]), _float_name(sends[0])
+    for r, t in enumerate(sends):
+        _expect(t, sends[0].shape, sends[0].dtype, device, f"sends[{r}]")
+    return device, DTYPE[name], sends[0].shape[0], sends[0].shape[1]
+
+
+def orthogonalize_workspace(sends):
+    """A workspace for orthogonalize_tensors of matrices shaped like these."""
+    import torch
+    device, dt, rows, cols = _ortho_shapes(sends)
+    with torch.cuda.device(device):
+        e, n = orthogonalize_workspace_raw(len(sends), rows, cols, dt)
+        return _allocate(e, n, device, "emu_orthogonalize_workspace")
+
+
+def orthogonalize_tensors(sends, recvs, steps: int = 5, coeffs=None, workspace=None, stream=None) -> None:
+    """emu_orthogonalize: ``steps`` Newton-Schulz steps on every rank's matrix
+    ``sends[r]`` into ``recvs[r]`` (in place allowed).  ``coeffs``: None, one
+    triple (a, b, c) for every step, or one triple per step."""
+    device, dt, rows, cols = _ortho_shapes(sends)
+    if len(recvs) != len(sends):
+        raise ValueError("need one send and one receive matrix per rank")
+    for r, t in enumerate(recvs):
+        _expect(t, sends[0].shape, sends[0].dtype, device, f"recvs[{r}]")
+    if coeffs is not None:
+        flat = [float(v) for c in coeffs for v in (c if hasattr(c, "__len__") else (c,))]
+        if len(flat) == 3:
+            flat = flat * max(int(steps), 1)
+        if len(flat) != 3 * steps:
+            raise ValueError("coeffs: one triple, or one per step")
+        coeffs = flat
+    with _Launch(device, stream, workspace, lambda: orthogonalize_workspace_raw(len(sends), rows, cols, dt),
+                 "emu_orthogonalize_workspace") as c:
+        _check(orthogonalize_raw([t.data_ptr() for t in sends], [t.data_ptr() for t in recvs], rows, cols, steps,
+                                 coeffs, dt, c.ptr, c.bytes, c.stream), "emu_orthogonalize")

@@ -415,6 +415,123 @@ int emu_buffer_layout(size_t nbufs, size_t bytes, size_t offsets[], size_t* pool
 #define EMU_STREAM_COPY 2
 int emu_stream_probe(int kind, const void* src, void* dst, size_t bytes, void* stream);
 
+/*
+ * Operators of a sharded training step, over `nranks` virtual ranks whose
+ * buffers live on one GPU: what forms the gradients that the collectives
+ * reduce, and what turns a reduced gradient into an update.  They join
+ * statistics over the ranks (a maximum and a sum per token, counts and sums
+ * per expert) in ascending rank order, so a call repeats bit for bit.  They
+ * need no communicator; nranks is 1..EMU_MAX_RANKS.
+ *
+ * Common rules.  The calls only enqueue kernels on `stream` of the current
+ * device, which must hold the buffers: no allocation, copy, memset or
+ * synchronisation, so a first call may be captured in a HIP graph too.
+ * Device memory that a call works in is the caller's: the *_workspace
+ * functions give its size (host arithmetic only, the same for equal
+ * arguments; it depends on the number of CUs of the current device), its
+ * contents before and after a call mean nothing, and calls (or replays of
+ * captured graphs) that may overlap in time need a workspace each.
+ * Host arrays (of pointers or sizes) are read during the call only.  Device
+ * pointers are non-NULL, except where a size is 0 or NULL is allowed, and
+ * 16-byte aligned; matrices are dense and row-major.  Outputs and the
+ * workspace must not overlap any other buffer of the call, except where in
+ * place is allowed.  dtype is EMU_FLOAT32, EMU_FLOAT16 or EMU_BFLOAT16.
+ * Errors, checked before anything is enqueued: EMU_ERR_INVALID_ARGUMENT
+ * (also for a workspace that is too small); EMU_ERR_HIP for a launch failure.
+ */
+
+/*
+ * emu_cross_entropy - softmax cross entropy of `tokens` hidden states x
+ * [tokens][dim] against an output projection whose rows (one per word of the
+ * vocabulary) are split over the ranks: w[r] is [vocab[r]][dim], and rank r's
+ * first row has index vocab[0] + .. + vocab[r-1].  With z_tv = x_t . w_v:
+ *   lse[t]  = log sum_v exp z_tv             (f32, natural logarithm)
+ *   loss[t] = lse[t] - z_t,targets[t]        (f32)
+ * The logits are not kept: a pass over them leaves a maximum and a sum per
+ * token and tile of rows.  A target outside [0, sum of vocab) marks a token
+ * without a loss: its loss is 0 (its lse is still formed).
+ *   targets  int64, device; dim * element size must be a multiple of 16
+ *   vocab    any sizes, 0 allowed (w[r] is then not read); at least one row
+ *            in all; tokens == 0 is a successful no-op (its dw: zeros)
+ * Products are summed in f32.  Limits: tokens <= 2^20, dim <= 2^16,
+ * vocabulary <= 2^24 rows, tokens * vocabulary <= 2^37.
+ *
+ * emu_cross_entropy_grad - the gradients, for dloss[t] = d L / d loss[t]
+ * (f32) and the lse of a forward call:
+ *   g_tv = dloss[t] (exp(z_tv - lse[t]) - [v = targets[t]]), 0 without a loss
+ *   dx = g w (over all ranks),  dw[r] = g_r^T x
+ * in dtype, rounded once from f32 sums; g itself is rounded to dtype before
+ * these products (f16: after scaling by a power of two that follows the
+ * largest |dloss|).  A token without a loss adds nothing to dw, whatever its
+ * hidden state holds, and its row of dx is 0.  dx or dw may be NULL (not
+ * wanted; not both); dw[r] of a rank with rows must not be NULL if dw is
+ * given.
+ *
+ * emu_cross_entropy_workspace - bytes for either call: want_dx and want_dw 0
+ * for emu_cross_entropy, else which gradients emu_cross_entropy_grad forms.
+ */
+int emu_cross_entropy_workspace(int nranks, const size_t vocab[], size_t tokens, size_t dim, int dtype, int want_dx,
+                                int want_dw, size_t* bytes);
+int emu_cross_entropy(int nranks, const void* x, const void* const w[], const size_t vocab[],
+                      const long long* targets, size_t tokens, size_t dim, float* loss, float* lse, int dtype,
+                      void* workspace, size_t workspace_bytes, void* stream);
+int emu_cross_entropy_grad(int nranks, const void* x, const void* const w[], const size_t vocab[],
+                           const long long* targets, const float* lse, const float* dloss, size_t tokens, size_t dim,
+                           void* dx, void* const dw[], int dtype, void* workspace, size_t workspace_bytes,
+                           void* stream);
+
+/*
+ * emu_balance_loss - the load-balance loss of a mixture-of-experts router over
+ * every rank's tokens, the number of tokens each expert was chosen by, and
+ * the gradient of the router's logits.  Rank r has tokens[r] rows of
+ * `nexperts` logits and, for each row, the `topk` experts that were chosen
+ * (int32; an entry outside [0, nexperts) was dropped and counts nowhere).  A
+ * row without any chosen expert is padding: it takes no part, and its
+ * gradients are 0.  With p the softmax of a row, N the rows that take part,
+ * over all ranks:
+ *   f_e  = (choices of e) / (N * topk),  P_e = (1/N) sum p_e
+ *   loss = coef * nexperts * sum_e f_e P_e          (f32; 0 if N = 0)
+ *   dlogits = coef * nexperts / N * p_e (f_e - sum_e' f_e' p_e')
+ * (f carries no gradient).  A row whose logits are all -infinity has no
+ * probabilities: it adds nothing to P and its gradients are 0.
+ *   counts   int64 [nranks + 1][nexperts]: each rank's choices, then their sum
+ *   dlogits  NULL, or per rank [tokens[r]][nexperts] in dtype
+ *   nexperts 1..EMU_MAX_EXPERTS;  topk 1..nexperts;  tokens[r] <= 2^24 (0
+ *            allowed: that rank's pointers are not read);  coef finite
+ */
+#define EMU_MAX_EXPERTS 1024
+int emu_balance_loss_workspace(int nranks, const size_t tokens[], size_t nexperts, size_t* bytes);
+int emu_balance_loss(int nranks, const void* const logits[], const int* const experts[], const size_t tokens[],
+                     size_t nexperts, size_t topk, float coef, long long* counts, float* loss,
+                     void* const dlogits[], int dtype, void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * emu_orthogonalize - Newton-Schulz orthogonalisation of one matrix per rank,
+ * as an orthogonalising optimiser applies it to the (reduce-scattered)
+ * gradient that each rank holds before the updates are all-gathered:
+ *   X_0 = G / (|G|_F + 1e-7)
+ *   X <- a X + b (X X^T) X + c (X X^T)^2 X      (`steps` times)
+ * (a tall G is treated as its transpose).  sendbufs[r] and recvbufs[r] are
+ * [rows][cols]; in place (recvbufs[r] == sendbufs[r]) is allowed.
+ *   steps   1..EMU_MAX_ORTHO_STEPS
+ *   coeffs  host array of steps triples (a, b, c), or NULL for
+ *           (3.4445, -4.7750, 2.0315) in every step, which brings singular
+ *           values into about [0.7, 1.2] in 5 steps
+ * X is held in 22 significand bits from step to step and products are summed
+ * in f32; factors have 22 bits for f32 and f16 matrices, 11 bits for bf16
+ * ones.  Entries of X, X X^T and b X X^T + c (X X^T)^2 must stay below 63 in
+ * magnitude (the default coefficients keep them below 4), else the result
+ * holds infinities or NaN.  A matrix of zeros gives zeros; one with an
+ * infinity or NaN gives NaN throughout.
+ * rows, cols: 1 to 2^20 each, at most 2^32 elements; a size of 0 is a
+ * successful no-op.
+ */
+#define EMU_MAX_ORTHO_STEPS 16
+int emu_orthogonalize_workspace(int nranks, size_t rows, size_t cols, int dtype, size_t* bytes);
+int emu_orthogonalize(int nranks, const void* const sendbufs[], void* const recvbufs[], size_t rows, size_t cols,
+                      int steps, const float* coeffs, int dtype, void* workspace, size_t workspace_bytes,
+                      void* stream);
+
 /* emu_strerror - static description of a result code (never NULL). */
 const char* emu_strerror(int code);
 

@@ -16,6 +16,7 @@ of one step, so that a reader can check every fold against the text:
 * ``tree``      - tree reduce-up / broadcast-down simulator.
 * ``allreduce`` - the whole all-reduce over N virtual ranks, plus the fp64
   reference sum and the normwise tolerance check.
+* ``train``     - the training-step operators in float64 (not from the pages).
 
 Parity status of every function is stated in its module header.
 """
