@@ -18,9 +18,11 @@
 // they are stored times 2^10, so that the lo parts stay clear of f16's
 // smallest steps (2^-24) and values up to 63 fit.
 //
-// Layout.  X is kept row-major and transposed (both products then read
-// k-contiguous rows), A and B are symmetric: only tiles on and below the
-// diagonal are computed and each is written twice.
+// Layout.  X lies row-major, once: the product with itself reads its rows, the
+// product with B its columns.  A and B are symmetric: only tiles on and below
+// the diagonal are computed, and each is written twice.  Pairs lie as tile.h
+// wants them, in blocks of 32 hi and 32 lo; without pairs the lo part of X
+// has an array of its own, which only the a X term reads.
 #include "tile.h"
 #include "train.h"
 
@@ -48,74 +50,104 @@ __device__ __forceinline__ void split(float v, _Float16& hi, _Float16& lo) {
 }
 
 // |G|^2 of each matrix in parts, in 64 bits (the square of a large f32 has no
-// f32 value).  Workgroup (x, y): share x of matrix y.
-constexpr int kNormParts = 64;
+// f32 value).  Workgroup (x, y): share x of matrix y, 16 bytes a lane.
 template <DType T>
 __global__ __launch_bounds__(256) void ortho_norm(OrthoArgs a, double* __restrict__ parts) {
   typedef typename Elem<T>::type E;
-  const uint64_t count = (uint64_t)a.rows * a.cols;
+  constexpr int V = Unit<T>::elems;
+  typedef E EV __attribute__((ext_vector_type(V)));
+  const uint64_t count = (uint64_t)a.rows * a.cols, vecs = count / V;
   const E* in = static_cast<const E*>(a.in[blockIdx.y]);
   double s = 0.0;
-  for (uint64_t i = (uint64_t)blockIdx.x * 256 + threadIdx.x; i < count; i += (uint64_t)gridDim.x * 256) {
-    const double v = (double)(float)in[i];
+  for (uint64_t i = (uint64_t)blockIdx.x * 256 + threadIdx.x; i < vecs; i += (uint64_t)gridDim.x * 256) {
+    const EV x = reinterpret_cast<const EV*>(in)[i];
+#pragma unroll
+    for (int e = 0; e < V; ++e) s += (double)(float)x[e] * (double)(float)x[e];
+  }
+  if (blockIdx.x == 0 && threadIdx.x < count - vecs * V) {
+    const double v = (double)(float)in[vecs * V + threadIdx.x];
     s += v * v;
   }
   for (int d = 1; d < 64; d <<= 1) s += __shfl_xor(s, d);
   __shared__ double w[4];
   if ((threadIdx.x & 63) == 0) w[threadIdx.x >> 6] = s;
   __syncthreads();
-  if (threadIdx.x == 0) parts[blockIdx.y * kNormParts + blockIdx.x] = w[0] + w[1] + w[2] + w[3];
+  if (threadIdx.x == 0) parts[blockIdx.y * gridDim.x + blockIdx.x] = w[0] + w[1] + w[2] + w[3];
 }
 
-// One matrix's state.  Pitches are whole 16-byte vectors; what lies past the
-// last column is zero.
+// One matrix's state: byte offsets, and pitches in bytes.  What lies past the
+// last column of a row is zero.
 struct OrthoMat {
-  uint64_t x[2], xt[2], a, b;      // byte offsets of the hi part; the lo part follows at + lo_x / lo_a
-  uint64_t lo_x, lo_xt, lo_a;
+  uint64_t x[2], lo[2], a, b;      // lo: without pairs
   uint64_t bytes;                  // per matrix
-  uint32_t m, n, mp, np;
+  uint32_t m, n, xp, ap;           // X is [m][n] with pitch xp, A and B [m][m] with pitch ap
+  uint32_t parts;
 };
 
-// X_0 = G / (|G| + 1e-7), both layouts.  64 x 64 tiles of X; a tall G is read
-// transposed.
-template <DType T>
+// Byte offset of column c in a row.
+template <bool PAIR>
+__device__ __forceinline__ uint32_t column(uint32_t c) {
+  return PAIR ? (c >> 5) * 128 + (c & 31) * 2 : c * 2;
+}
+
+// Four consecutive values (c a multiple of 4), stored as hi + lo.
+template <bool PAIR>
+__device__ __forceinline__ void put(char* row, char* lo_row, uint32_t c, const float (&v)[4]) {
+  f16x4 hi, lo;
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    _Float16 h, l;
+    split(v[e], h, l);
+    hi[e] = h;
+    lo[e] = l;
+  }
+  *reinterpret_cast<f16x4*>(row + column<PAIR>(c)) = hi;
+  if (PAIR) *reinterpret_cast<f16x4*>(row + column<PAIR>(c) + 64) = lo;
+  else if (lo_row) *reinterpret_cast<f16x4*>(lo_row + c * 2) = lo;
+}
+// hi + lo of four consecutive values (without pairs and lo_row: hi).
+template <bool PAIR>
+__device__ __forceinline__ void get(const char* row, const char* lo_row, uint32_t c, float (&v)[4]) {
+  const f16x4 hi = *reinterpret_cast<const f16x4*>(row + column<PAIR>(c));
+  f16x4 lo = {};
+  if (PAIR) lo = *reinterpret_cast<const f16x4*>(row + column<PAIR>(c) + 64);
+  else if (lo_row) lo = *reinterpret_cast<const f16x4*>(lo_row + c * 2);
+#pragma unroll
+  for (int e = 0; e < 4; ++e) v[e] = (float)hi[e] + (float)lo[e];
+}
+
+// X_0 = G / (|G| + 1e-7).  64 x 64 tiles of X; a tall G is read transposed.
+// Columns up to the pitch's end become zeros.
+template <DType T, bool PAIR>
 __global__ __launch_bounds__(256) void ortho_load(OrthoArgs a, OrthoMat q, const double* __restrict__ parts,
                                                   char* __restrict__ ws) {
   typedef typename Elem<T>::type E;
   constexpr int B = 64;
   __shared__ float tile[B][B + 1];
   double s = 0.0;
-  for (int i = 0; i < kNormParts; ++i) s += parts[blockIdx.z * kNormParts + i];
+  for (uint32_t i = threadIdx.x & 63; i < q.parts; i += 64) s += parts[blockIdx.z * q.parts + i];
+  for (int d = 1; d < 64; d <<= 1) s += __shfl_xor(s, d);
   // an infinite or NaN entry makes the whole result NaN (the sum of finite
   // squares stays far inside f64's range)
   const double inv = s < (double)INFINITY ? (double)kScale / (sqrt(s) + 1e-7) : (double)NAN;
   const E* in = static_cast<const E*>(a.in[blockIdx.z]);
   char* base = ws + blockIdx.z * q.bytes;
-  const uint32_t r0 = blockIdx.y * B, c0 = blockIdx.x * B, x = threadIdx.x % B, y = threadIdx.x / B;   // of G
-  for (uint32_t i = y; i < B; i += 4)
-    tile[i][x] = r0 + i < a.rows && c0 + x < a.cols
-                     ? (float)((double)(float)in[(uint64_t)(r0 + i) * a.cols + c0 + x] * inv)
-                     : 0.0f;
-  __syncthreads();
   const bool tall = a.rows > a.cols;
-  // the layout G has, and the other one
-  const uint64_t same = tall ? q.xt[0] : q.x[0], other = tall ? q.x[0] : q.xt[0];
-  const uint64_t lo_same = tall ? q.lo_xt : q.lo_x, lo_other = tall ? q.lo_x : q.lo_xt;
-  const uint32_t p_same = tall ? q.mp : q.np, p_other = tall ? q.np : q.mp;
+  const uint32_t r0 = blockIdx.y * B, c0 = blockIdx.x * B;        // of X
+  const uint32_t g0 = tall ? c0 : r0, h0 = tall ? r0 : c0;         // of G
+  const uint32_t x = threadIdx.x % B, y = threadIdx.x / B;
   for (uint32_t i = y; i < B; i += 4) {
-    _Float16 hi, lo;
-    if (r0 + i < a.rows && c0 + x < p_same) {
-      split(tile[i][x], hi, lo);
-      _Float16* at = reinterpret_cast<_Float16*>(base + same) + (uint64_t)(r0 + i) * p_same + c0 + x;
-      at[0] = hi;
-      at[lo_same / 2] = lo;
-    }
-    if (c0 + i < a.cols && r0 + x < p_other) {
-      split(tile[x][i], hi, lo);
-      _Float16* at = reinterpret_cast<_Float16*>(base + other) + (uint64_t)(c0 + i) * p_other + r0 + x;
-      at[0] = hi;
-      at[lo_other / 2] = lo;
-    }
+    float v = 0.0f;
+    if (g0 + i < a.rows && h0 + x < a.cols) v = (float)((double)(float)in[(uint64_t)(g0 + i) * a.cols + h0 + x] * inv);
+    if (tall) tile[x][i] = v;
+    else tile[i][x] = v;
+  }
+  __syncthreads();
+  const uint32_t width = q.xp / (PAIR ? 4 : 2), c = threadIdx.x % 16 * 4;
+  for (uint32_t i = threadIdx.x / 16; i < B; i += 16) {
+    if (r0 + i >= q.m || c0 + c >= width) continue;
+    const float v[4] = {tile[i][c], tile[i][c + 1], tile[i][c + 2], tile[i][c + 3]};
+    put<PAIR>(base + q.x[0] + (uint64_t)(r0 + i) * q.xp, base + q.lo[0] + (uint64_t)(r0 + i) * q.xp, c0 + c, v);
   }
 }
 
@@ -125,26 +157,6 @@ __device__ __forceinline__ void triangle(uint32_t t, uint32_t& i, uint32_t& j) {
   while (i * (i + 1) / 2 > t) --i;
   while ((i + 1) * (i + 2) / 2 <= t) ++i;
   j = t - i * (i + 1) / 2;
-}
-
-// P * Q^T over k: with pairs, hi hi + hi lo + lo hi.
-template <class K, bool PAIR>
-__device__ __forceinline__ void product(const char* p, uint64_t lo_p, uint32_t rows_p, const char* q, uint64_t lo_q,
-                                        uint32_t rows_q, uint32_t pitch, uint32_t lds, typename K::Acc& acc) {
-  const uint32_t ld = pitch * 2;
-  Operand a{p, ld, (int)rows_p}, b{q, ld, (int)rows_q};
-  if constexpr (PAIR) {
-    // the small products first
-    a.base = p + lo_p;
-    K::run(a, b, ld, lds, acc);
-    __syncthreads();
-    a.base = p;
-    b.base = q + lo_q;
-    K::run(a, b, ld, lds, acc);
-    __syncthreads();
-    b.base = q;
-  }
-  K::run(a, b, ld, lds, acc);
 }
 
 // What a symmetric product does with its tile.  kGram: A = X X^T;
@@ -159,48 +171,39 @@ __global__ __launch_bounds__(K::threads) void ortho_sym(OrthoMat q, char* ws, ui
   char* base = ws + blockIdx.y * q.bytes;
   const uint32_t r0 = ti * K::BM, c0 = tj * K::BN;
   typename K::Acc acc = {};
-  const uint32_t pitch = KIND == kGram ? q.np : q.mp;
+  const uint32_t pitch = KIND == kGram ? q.xp : q.ap;
   const char* src = base + (KIND == kGram ? q.x[cur] : q.a);
-  const uint64_t lo = KIND == kGram ? q.lo_x : q.lo_a;
-  product<K, PAIR>(src + (uint64_t)r0 * pitch * 2, lo, q.m - r0, src + (uint64_t)c0 * pitch * 2, lo, q.m - c0, pitch,
-                   lds_address(lds), acc);
+  const Operand a{src + (uint64_t)r0 * pitch, pitch, (int)(q.m - r0)}, b{src + (uint64_t)c0 * pitch, pitch, (int)(q.m - c0)};
+  K::run(a, b, KIND == kGram ? q.n : q.m, lds_address(lds), acc);
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, wm = wave / K::WGN, wn = wave % K::WGN;
-  _Float16* out = reinterpret_cast<_Float16*>(base + (KIND == kGram ? q.a : q.b));
-  const _Float16* am = reinterpret_cast<const _Float16*>(base + q.a);
-  const uint64_t lo_a = q.lo_a / 2;
+  char* out = base + (KIND == kGram ? q.a : q.b);
+  const uint32_t width = q.ap / (PAIR ? 4 : 2);
 #pragma unroll
   for (int j = 0; j < K::NF; ++j) {
     const uint32_t c = c0 + wn * K::WN + j * 16 + (lane & 15);
 #pragma unroll
     for (int i = 0; i < K::MF; ++i) {
       const uint32_t r = r0 + wm * K::WM + i * 16 + 4 * (lane >> 4);
-      // row c, columns r .. r + 3 (the upper part), and its mirror
-      if (c >= q.m || r >= q.mp) continue;
-      const uint64_t at = (uint64_t)c * q.mp + r;
-      f16x4 hi, lw;
-      f16x4 ahi = {}, alo = {};
-      if (KIND == kPoly) {
-        ahi = *reinterpret_cast<const f16x4*>(am + at);
-        if (PAIR) alo = *reinterpret_cast<const f16x4*>(am + lo_a + at);
-      }
+      // row c, columns r .. r + 3 (on and above the diagonal), and its mirror
+      if (c >= q.m || r >= width) continue;
+      float v[4], old[4];
+      if (KIND == kPoly) get<PAIR>(base + q.a + (uint64_t)c * q.ap, nullptr, r, old);
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
-        float v = acc[i][j][e] * kInvScale;
-        if (KIND == kPoly) v = cb * ((float)ahi[e] + (float)alo[e]) + cc * v;
-        if (r + e >= q.m) v = 0.0f;
-        _Float16 h, l;
-        split(v, h, l);
-        hi[e] = h;
-        lw[e] = l;
+        v[e] = acc[i][j][e] * kInvScale;
+        if (KIND == kPoly) v[e] = cb * old[e] + cc * v[e];
+        if (r + e >= q.m) v[e] = 0.0f;
       }
-      *reinterpret_cast<f16x4*>(out + at) = hi;
-      if (PAIR) *reinterpret_cast<f16x4*>(out + lo_a + at) = lw;
+      put<PAIR>(out + (uint64_t)c * q.ap, nullptr, r, v);
       if (ti != tj) {
 #pragma unroll
         for (int e = 0; e < 4; ++e)
           if (r + e < q.m) {
-            out[(uint64_t)(r + e) * q.mp + c] = hi[e];
-            if (PAIR) out[lo_a + (uint64_t)(r + e) * q.mp + c] = lw[e];
+            _Float16 h, l;
+            split(v[e], h, l);
+            char* at = out + (uint64_t)(r + e) * q.ap + column<PAIR>(c);
+            *reinterpret_cast<_Float16*>(at) = h;
+            if (PAIR) *reinterpret_cast<_Float16*>(at + 64) = l;
           }
       }
     }
@@ -208,7 +211,7 @@ __global__ __launch_bounds__(K::threads) void ortho_sym(OrthoMat q, char* ws, ui
 }
 
 // X' = a X + B X into the other buffers, or, in the last step, into the
-// output.  First operand B (rows i), second X transposed (rows k).
+// output.  First operand X as columns of k, second B (rows).
 template <DType T, class K, bool PAIR, bool LAST>
 __global__ __launch_bounds__(K::threads) void ortho_step(OrthoArgs a, OrthoMat q, char* ws, uint32_t cur, float ca,
                                                          uint32_t tm, uint32_t tn) {
@@ -217,82 +220,69 @@ __global__ __launch_bounds__(K::threads) void ortho_step(OrthoArgs a, OrthoMat q
   uint32_t m, n;
   tile_of(blockIdx.x, tm, tn, 8, m, n);
   char* base = ws + blockIdx.y * q.bytes;
-  const uint32_t r0 = m * K::BM, c0 = n * K::BN;
+  const uint32_t c0 = m * K::BM, r0 = n * K::BN;
   typename K::Acc acc = {};
-  product<K, PAIR>(base + q.b + (uint64_t)r0 * q.mp * 2, q.lo_a, q.m - r0,
-                   base + q.xt[cur] + (uint64_t)c0 * q.mp * 2, q.lo_xt, q.n - c0, q.mp, lds_address(lds), acc);
+  const Operand x{base + q.x[cur] + (uint64_t)c0 * (PAIR ? 4 : 2), q.xp, (int)(q.n - c0)};
+  const Operand b{base + q.b + (uint64_t)r0 * q.ap, q.ap, (int)(q.m - r0)};
+  K::run(x, b, q.m, lds_address(lds), acc);
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, wm = wave / K::WGN, wn = wave % K::WGN;
-  const _Float16* xt = reinterpret_cast<const _Float16*>(base + q.xt[cur]);
-  _Float16* nxt = reinterpret_cast<_Float16*>(base + q.xt[cur ^ 1]);
-  _Float16* nx = reinterpret_cast<_Float16*>(base + q.x[cur ^ 1]);
   E* out = static_cast<E*>(a.out[blockIdx.y]);
   const bool tall = a.rows > a.cols;
+  const uint32_t width = q.xp / (PAIR ? 4 : 2);
 #pragma unroll
   for (int j = 0; j < K::NF; ++j) {
-    const uint32_t k = c0 + wn * K::WN + j * 16 + (lane & 15);
+    const uint32_t r = r0 + wn * K::WN + j * 16 + (lane & 15);
+    const uint64_t row = (uint64_t)r * q.xp;
 #pragma unroll
     for (int i = 0; i < K::MF; ++i) {
-      const uint32_t r = r0 + wm * K::WM + i * 16 + 4 * (lane >> 4);
-      if (r >= q.mp || k >= q.np) continue;
-      f16x4 xh = {}, xl = {};
-      if (k < q.n) {
-        xh = *reinterpret_cast<const f16x4*>(xt + (uint64_t)k * q.mp + r);
-        xl = *reinterpret_cast<const f16x4*>(xt + q.lo_xt / 2 + (uint64_t)k * q.mp + r);
-      }
-      f16x4 hi, lw;
+      const uint32_t c = c0 + wm * K::WM + i * 16 + 4 * (lane >> 4);
+      if (r >= q.m || c >= width) continue;
       float v[4];
+      get<PAIR>(base + q.x[cur] + row, base + q.lo[cur] + row, c, v);
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
-        v[e] = ca * ((float)xh[e] + (float)xl[e]) + acc[i][j][e] * kInvScale;
-        if (r + e >= q.m || k >= q.n) v[e] = 0.0f;
-        _Float16 h, l;
-        split(v[e], h, l);
-        hi[e] = h;
-        lw[e] = l;
+        v[e] = ca * v[e] + acc[i][j][e] * kInvScale;
+        if (c + e >= q.n) v[e] = 0.0f;
       }
       if constexpr (LAST) {
 #pragma unroll
         for (int e = 0; e < 4; ++e)
-          if (r + e < q.m && k < q.n)
-            out[tall ? (uint64_t)k * a.cols + r + e : (uint64_t)(r + e) * a.cols + k] = (E)(v[e] * kInvScale);
+          if (c + e < q.n) out[tall ? (uint64_t)(c + e) * a.cols + r : (uint64_t)r * a.cols + c + e] = (E)(v[e] * kInvScale);
       } else {
-        if (k < q.n) {
-          *reinterpret_cast<f16x4*>(nxt + (uint64_t)k * q.mp + r) = hi;
-          *reinterpret_cast<f16x4*>(nxt + q.lo_xt / 2 + (uint64_t)k * q.mp + r) = lw;
-        }
-#pragma unroll
-        for (int e = 0; e < 4; ++e)
-          if (r + e < q.m) {
-            nx[(uint64_t)(r + e) * q.np + k] = hi[e];
-            if (PAIR) nx[q.lo_x / 2 + (uint64_t)(r + e) * q.np + k] = lw[e];
-          }
+        put<PAIR>(base + q.x[cur ^ 1] + row, base + q.lo[cur ^ 1] + row, c, v);
       }
     }
   }
 }
 
-typedef TileMma<DType::F16, 256, 256, 2, 4> Big;
-typedef TileMma<DType::F16, 128, 128, 2, 2> Mid;
+template <bool PAIR, OperandKind A>
+using Big = TileMma<DType::F16, 256, 256, 2, 4, A, kRows, PAIR>;
+template <bool PAIR, OperandKind A>
+using Mid = TileMma<DType::F16, 128, 128, 2, 2, A, kRows, PAIR>;
+template <bool PAIR, OperandKind A>
+using Small = TileMma<DType::F16, 64, 64, 2, 2, A, kRows, PAIR>;
+
+bool pairs(DType t) { return t != DType::BF16; }
 
 OrthoMat layout(const OrthoArgs& a) {
   OrthoMat q{};
   q.m = std::min(a.rows, a.cols);
   q.n = std::max(a.rows, a.cols);
-  q.mp = (uint32_t)align_up(q.m, 8);
-  q.np = (uint32_t)align_up(q.n, 8);
+  const bool p = pairs(a.type);
+  q.xp = (uint32_t)(p ? align_up(q.n, 32) * 4 : align_up(q.n, 8) * 2);
+  q.ap = (uint32_t)(p ? align_up(q.m, 32) * 4 : align_up(q.m, 8) * 2);
   size_t at = 0;
-  auto take = [&](size_t n) { const size_t p = at; at = align_up(at + n, 256); return p; };
-  const size_t x = (size_t)q.m * q.np * 2, xt = (size_t)q.n * q.mp * 2, s = (size_t)q.m * q.mp * 2;
-  q.lo_x = align_up(x, 256);
-  q.lo_xt = align_up(xt, 256);
-  q.lo_a = align_up(s, 256);
+  auto take = [&](size_t n) { const size_t o = at; at = align_up(at + n, 256); return o; };
   for (int i = 0; i < 2; ++i) {
-    q.x[i] = take(2 * q.lo_x);
-    q.xt[i] = take(2 * q.lo_xt);
+    q.x[i] = take((size_t)q.m * q.xp);
+    if (!p) q.lo[i] = take((size_t)q.m * q.xp);
   }
-  q.a = take(2 * q.lo_a);
-  q.b = take(2 * q.lo_a);
+  q.a = take((size_t)q.m * q.ap);
+  q.b = take((size_t)q.m * q.ap);
   q.bytes = at;
+  // 32 KiB of a matrix per workgroup at least, and enough of them for the CUs
+  const uint64_t most = (uint64_t)q.m * q.n * elem_size(a.type) / 32768 + 1;
+  q.parts = (uint32_t)std::min<uint64_t>(most, std::max<uint64_t>(1, 8u * a.cus / a.nranks));
   return q;
 }
 
@@ -305,7 +295,7 @@ void launch_sym(const OrthoMat& q, uint32_t nmat, char* ws, uint32_t cur, float 
 }
 template <DType T, class K, bool PAIR>
 void launch_step(const OrthoArgs& a, const OrthoMat& q, char* ws, uint32_t cur, float ca, bool last, hipStream_t s) {
-  const uint32_t tm = ceil_div(q.m, K::BM), tn = ceil_div(q.n, K::BN);
+  const uint32_t tm = ceil_div(q.n, K::BM), tn = ceil_div(q.m, K::BN);
   if (last)
     hipLaunchKernelGGL((ortho_step<T, K, PAIR, true>), dim3(tm * tn, a.nranks), dim3(K::threads), 0, s, a, q, ws, cur,
                        ca, tm, tn);
@@ -314,30 +304,48 @@ void launch_step(const OrthoArgs& a, const OrthoMat& q, char* ws, uint32_t cur, 
                        ca, tm, tn);
 }
 
+// The largest tile that still gives every CU one.
+enum Shape { kBig, kMid, kSmall };
+template <class F>
+Shape shape_of(int cus, uint32_t nmat, F tiles) {
+  if ((uint64_t)tiles(256u) * nmat >= (uint64_t)cus) return kBig;
+  return (uint64_t)tiles(128u) * nmat >= (uint64_t)cus ? kMid : kSmall;
+}
+
 template <DType T>
 hipError_t run(const OrthoArgs& a, char* workspace, hipStream_t s) {
   constexpr bool PAIR = T != DType::BF16;
   const OrthoMat q = layout(a);
   double* parts = reinterpret_cast<double*>(workspace);
-  char* ws = workspace + align_up((size_t)a.nranks * kNormParts * sizeof(double), 256);
-  hipLaunchKernelGGL(ortho_norm<T>, dim3(kNormParts, a.nranks), dim3(256), 0, s, a, parts);
-  hipLaunchKernelGGL(ortho_load<T>, dim3(ceil_div(a.cols, 64), ceil_div(a.rows, 64), a.nranks), dim3(256), 0, s, a, q,
-                     parts, ws);
-  const uint64_t t = ceil_div(q.m, 256);
-  const bool sym_big = t * (t + 1) / 2 * a.nranks >= (uint64_t)a.cus;
-  const bool step_big = t * ceil_div(q.n, 256) * a.nranks >= (uint64_t)a.cus;
+  char* ws = workspace + align_up((size_t)a.nranks * q.parts * sizeof(double), 256);
+  hipLaunchKernelGGL(ortho_norm<T>, dim3(q.parts, a.nranks), dim3(256), 0, s, a, parts);
+  hipLaunchKernelGGL((ortho_load<T, PAIR>), dim3(ceil_div(q.xp / (PAIR ? 4 : 2), 64), ceil_div(q.m, 64), a.nranks), dim3(256),
+                     0, s, a, q, parts, ws);
+  const Shape sym = shape_of(a.cus, a.nranks, [&](uint32_t b) { const uint32_t t = ceil_div(q.m, b); return t * (t + 1) / 2; });
+  const Shape step = shape_of(a.cus, a.nranks, [&](uint32_t b) { return ceil_div(q.m, b) * ceil_div(q.n, b); });
   uint32_t cur = 0;
   for (int i = 0; i < a.steps; ++i, cur ^= 1) {
     const float* c = a.coeffs + 3 * i;
-    if (sym_big) {
-      launch_sym<Big, PAIR, kGram>(q, a.nranks, ws, cur, 0.0f, 0.0f, s);
-      launch_sym<Big, PAIR, kPoly>(q, a.nranks, ws, cur, c[1], c[2], s);
-    } else {
-      launch_sym<Mid, PAIR, kGram>(q, a.nranks, ws, cur, 0.0f, 0.0f, s);
-      launch_sym<Mid, PAIR, kPoly>(q, a.nranks, ws, cur, c[1], c[2], s);
+    const bool last = i + 1 == a.steps;
+    switch (sym) {
+      case kBig:
+        launch_sym<Big<PAIR, kRows>, PAIR, kGram>(q, a.nranks, ws, cur, 0.0f, 0.0f, s);
+        launch_sym<Big<PAIR, kRows>, PAIR, kPoly>(q, a.nranks, ws, cur, c[1], c[2], s);
+        break;
+      case kMid:
+        launch_sym<Mid<PAIR, kRows>, PAIR, kGram>(q, a.nranks, ws, cur, 0.0f, 0.0f, s);
+        launch_sym<Mid<PAIR, kRows>, PAIR, kPoly>(q, a.nranks, ws, cur, c[1], c[2], s);
+        break;
+      default:
+        launch_sym<Small<PAIR, kRows>, PAIR, kGram>(q, a.nranks, ws, cur, 0.0f, 0.0f, s);
+        launch_sym<Small<PAIR, kRows>, PAIR, kPoly>(q, a.nranks, ws, cur, c[1], c[2], s);
+        break;
     }
-    if (step_big) launch_step<T, Big, PAIR>(a, q, ws, cur, c[0], i + 1 == a.steps, s);
-    else launch_step<T, Mid, PAIR>(a, q, ws, cur, c[0], i + 1 == a.steps, s);
+    switch (step) {
+      case kBig: launch_step<T, Big<PAIR, kCols>, PAIR>(a, q, ws, cur, c[0], last, s); break;
+      case kMid: launch_step<T, Mid<PAIR, kCols>, PAIR>(a, q, ws, cur, c[0], last, s); break;
+      default: launch_step<T, Small<PAIR, kCols>, PAIR>(a, q, ws, cur, c[0], last, s); break;
+    }
   }
   return hipGetLastError();
 }
@@ -345,7 +353,8 @@ hipError_t run(const OrthoArgs& a, char* workspace, hipStream_t s) {
 }  // namespace
 
 size_t ortho_space(const OrthoArgs& a) {
-  return align_up((size_t)a.nranks * kNormParts * sizeof(double), 256) + (size_t)a.nranks * layout(a).bytes;
+  const OrthoMat q = layout(a);
+  return align_up((size_t)a.nranks * q.parts * sizeof(double), 256) + (size_t)a.nranks * q.bytes;
 }
 
 int orthogonalize(const OrthoArgs& a, char* workspace, void* stream) {

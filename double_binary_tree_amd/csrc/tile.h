@@ -1,20 +1,36 @@
-// Matrix tiles on the matrix cores: C[m][n] = sum_k A[m][k] * B[n][k] for one
-// workgroup's BM x BN tile, both operands k-contiguous, sums in f32.
+// Matrix tiles on the matrix cores: C[m][n] = sum_k A(m, k) B(n, k) for one
+// workgroup's BM x BN tile, sums in f32.  An operand lies in memory either as
+// rows of k (kRows: the k of one m are contiguous) or as columns (kCols: the m
+// of one k are contiguous); nothing is transposed in memory.
 //
-// Staging.  One k-step covers 128 bytes of every row (64 16-bit or 32 f32
-// values).  Rows go from global memory straight to LDS, 16 bytes a lane, one
-// 1 KiB wave access holding 8 rows; two stages alternate, so the loads of
-// step s + 1 run while step s is multiplied.  The 16-byte chunk c of row r
-// sits at chunk c ^ ((r >> 1) & 7): the 16 rows that a matrix instruction
-// reads at one chunk then cover all 64 banks once (a row spans 32 banks, so
-// rows r and r + 1 differ in the half, rows r and r + 2 in the chunk).  The
-// permutation is applied to the global address, since LDS is filled in lane
-// order.
+// Staging.  One k-step covers 128 bytes of k per row (64 16-bit or 32 f32
+// values), so a stage holds 128 bytes times BM + BN whatever the layout.  It
+// goes from global memory straight to LDS, 16 bytes a lane, 1 KiB a wave
+// access; two stages alternate, so the loads of step s + 1 run while step s is
+// multiplied.  LDS is filled in lane order, so the permutations below are
+// applied to the global addresses.
+//   kRows: a wave access holds 8 rows of 128 bytes.  The 16-byte chunk c of
+//     row r sits at chunk c ^ ((r >> 1) & 7): the 16 rows that a matrix
+//     instruction reads at one chunk then cover all 64 banks once (a row
+//     spans 32 banks, so rows r and r + 1 differ in the half, rows r and r + 2
+//     in the chunk).
+//   kCols: a stage holds the step's k, each with the tile's m side by side.
+//     16-bit fragments come through the LDS transpose read: of 16 lanes, lanes
+//     4j .. 4j + 3 read the 16 m (32 bytes) of one k, and lane i receives the
+//     four k of m = i.  A 32-byte window w of k-row r sits at window w ^ h(r),
+//     h taken so that the 8 windows that 32 lanes read together (k-rows j and
+//     8 + j, j = 0 .. 3) cover all banks once.
 //
-// Ragged edges.  Rows past the operand's last one read the last row again
-// (their results are dropped by the caller).  A k extent is a whole number
-// of 16-byte chunks; in a last step that is not whole the missing chunks are
-// loaded from the row's last chunk and overwritten by zeros in LDS.
+// Pairs (PAIR).  Numbers held as the sum of two f16, hi + lo, lie in blocks of
+// 32: 64 bytes of hi, then 64 bytes of lo.  A step then covers 32 k, and its
+// three products hi hi + hi lo + lo hi share one stage: two thirds of the
+// loads and LDS reads that three separate passes would take.
+//
+// Ragged edges.  Rows (kCols: 16-byte chunks of m) past the operand's last one
+// read the last again; their results are dropped by the caller.  In a last
+// step that is not whole, what lies past k is loaded from the last valid place
+// and overwritten by zeros in LDS; a kRows operand's last 16-byte chunk of k
+// must hold zeros past k itself.
 #pragma once
 
 #include "device_ops.h"
@@ -49,8 +65,11 @@ struct Mma<DType::F32> {
   }
 };
 
-// One operand of a tile: `base` is the tile's first row at k = 0 (uniform),
-// `ld` the row pitch in bytes, `rows` how many rows are left (>= 1).
+enum OperandKind { kRows, kCols };
+
+// One operand of a tile: `base` is the tile's first m at k = 0 (uniform), `ld`
+// the pitch in bytes of a row (kCols: of a k), `rows` how many m are left
+// (>= 1; kCols: in whole 16-byte chunks, or to the end of the last chunk).
 struct Operand {
   const char* base;
   uint32_t ld;
@@ -77,78 +96,177 @@ __device__ __forceinline__ uint32_t lds_address(const void* p) {
 __device__ __forceinline__ u32x4 lds_read(uint32_t at) { return *(const LdsVec*)(uintptr_t)at; }
 __device__ __forceinline__ void lds_write(uint32_t at, u32x4 v) { *(LdsVec*)(uintptr_t)at = v; }
 
+// Four k of one m per lane, as described at the top.
+typedef short i16x4 __attribute__((ext_vector_type(4)));
+__device__ __forceinline__ i16x4 lds_read_transposed(uint32_t at) {
+  typedef __attribute__((address_space(3))) i16x4 LdsQuad;
+  return __builtin_amdgcn_ds_read_tr16_b64_v4i16((LdsQuad*)(uintptr_t)at);
+}
+
+// One operand's part of a stage: BX of m, `waves` waves loading it.
+template <DType T, int BX, OperandKind KIND, bool PAIR, int WAVES>
+struct Side {
+  static constexpr int es = T == DType::F32 ? 4 : 2;
+  static constexpr int kstep = PAIR ? 32 : kStepBytes / es;         // k per step
+  static constexpr int bytes = BX * kStepBytes;
+  static constexpr int row_bytes = BX * (PAIR ? 4 : es);            // kCols: one k in LDS
+  static constexpr int loads = bytes / 1024 / WAVES;                // per wave and stage
+  static_assert(loads * 1024 * WAVES == bytes, "whole wave accesses");
+  static_assert(!PAIR || T == DType::F16, "pairs are f16");
+  static_assert(KIND == kRows || row_bytes <= 1024, "a k-row within a wave access");
+  static_assert(KIND == kRows || row_bytes >= 128, "four windows at least");
+
+  // Where window w of k-row r sits.
+  static __device__ __forceinline__ uint32_t window(uint32_t w, uint32_t r) {
+    if constexpr (row_bytes >= 256) return w ^ ((r & 3) | ((r >> 1) & 4));
+    else return w ^ (((r >> 1) & 1) | ((r >> 2) & 2));
+  }
+
+  // This lane's byte offset from the step's base for load l of wave `wave`,
+  // with `left` k in the step; returns whether the place lies past them.
+  static __device__ __forceinline__ bool place(const Operand& o, int wave, int lane, int l, int left, uint32_t& off) {
+    if constexpr (KIND == kRows) {
+      const int r = (wave * loads + l) * 8 + (lane >> 3), c = (lane & 7) ^ ((r >> 1) & 7);
+      const int chunks = PAIR ? 8 : min(8, (left * es + 15) / 16);
+      off = (uint32_t)min(r, o.rows - 1) * o.ld + 16u * (uint32_t)min(c, chunks - 1);
+      return c >= chunks;
+    } else {
+      const int b = lane * 16, r = (wave * loads + l) * (1024 / row_bytes) + b / row_bytes;
+      const uint32_t w = window((uint32_t)(b % row_bytes) / 32, (uint32_t)r);
+      const int col = (int)w * 32 + (b & 16), last = PAIR ? (o.rows + 31) / 32 * 128 - 16 : (o.rows * es + 15) / 16 * 16 - 16;
+      off = (uint32_t)min(r, left - 1) * o.ld + (uint32_t)min(col, last);
+      return r >= left;
+    }
+  }
+  static __device__ __forceinline__ uint64_t advance(const Operand& o) {
+    return KIND == kRows ? (uint64_t)kStepBytes : (uint64_t)kstep * o.ld;
+  }
+
+  // Addresses of fragment f (16 m) within the stage's part, before the stage's
+  // own offset: `at(f)`, and what is added for half kk of the step.
+  struct Frag {
+    uint32_t base, h;             // kRows: base; kCols: base and the window permutation
+    __device__ __forceinline__ Frag(int lane) {
+      const uint32_t i = lane & 15, g = lane >> 4;
+      if constexpr (KIND == kRows) {
+        base = i * kStepBytes;
+        h = (i >> 1) & 7;
+      } else if constexpr (es == 2) {
+        const uint32_t r = 8 * g + (i >> 2);
+        base = r * row_bytes + (i & 3) * 8;
+        h = window(0, r);
+      } else {
+        base = 4 * g * row_bytes + (i & 7) * 4;
+        h = (i >> 3) | (g << 8);
+      }
+    }
+    // kk: half of the step (16-bit: k 32 kk .. 32 kk + 31; f32: 16 kk ..; pairs: 0 hi, 1 lo)
+    __device__ __forceinline__ u32x4 read(uint32_t part, uint32_t f, int kk, int lane) const {
+      if constexpr (KIND == kRows) {
+        return lds_read(part + f * 16 * kStepBytes + base + (((uint32_t)kk * 4 + (lane >> 4)) ^ h) * 16);
+      } else if constexpr (es == 2) {
+        const uint32_t w = PAIR ? (f >> 1) * 4 + (f & 1) + 2 * kk : f;
+        const uint32_t at = part + base + (w ^ h) * 32 + (PAIR ? 0 : kk * 32 * row_bytes);
+        const i16x4 lo = lds_read_transposed(at), hi = lds_read_transposed(at + 4 * row_bytes);
+        return bits<u32x4>(__builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7));
+      } else {
+        u32x4 v;
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          const uint32_t r = 16 * kk + 4 * (h >> 8) + q;
+          v[q] = *(const __attribute__((address_space(3))) uint32_t*)(uintptr_t)(part + base + (16 * kk + q) * row_bytes +
+                                                                            window(2 * f + (h & 255), r) * 32);
+        }
+        return v;
+      }
+    }
+  };
+};
+
 // BM x BN by WGM x WGN waves, each wave MF x NF fragments of 16 x 16.
 // acc[i][j] of a lane holds C[m][n] at m = 16 i + 4 (lane >> 4) + e, n = 16 j
 // + (lane & 15) of the wave's part, e = 0 .. 3.
-template <DType T, int BM_, int BN_, int WGM_, int WGN_>
+template <DType T, int BM_, int BN_, int WGM_, int WGN_, OperandKind KA = kRows, OperandKind KB = kRows, bool PAIR = false>
 struct TileMma {
   static constexpr int BM = BM_, BN = BN_, WGM = WGM_, WGN = WGN_;
   static constexpr int waves = WGM * WGN, threads = 64 * waves;
   static constexpr int WM = BM / WGM, WN = BN / WGN, MF = WM / 16, NF = WN / 16;
-  static constexpr int stage_bytes = (BM + BN) * kStepBytes;
+  typedef Side<T, BM, KA, PAIR, waves> SA;
+  typedef Side<T, BN, KB, PAIR, waves> SB;
+  static constexpr int kstep = SA::kstep;
+  static constexpr int stage_bytes = SA::bytes + SB::bytes;
   static constexpr int lds_bytes = 2 * stage_bytes;
-  static constexpr int LA = BM / 8 / waves, LB = BN / 8 / waves;   // loads per wave and stage
-  static_assert(LA * 8 * waves == BM && LB * 8 * waves == BN, "whole wave accesses");
   using Acc = f32x4[MF][NF];
 
-  // Byte offset of this lane's chunk of load l (0 .. n-1 of the wave) from
-  // the operand's base at k = 0, and whether the chunk lies in `chunks`.
-  template <int L>
-  static __device__ __forceinline__ void offsets(const Operand& o, int wave, int lane, int chunks, uint32_t (&off)[L],
-                                                 bool (&pad)[L]) {
+  static __device__ __forceinline__ void multiply(uint32_t lds, int wm, int wn, int lane, const typename SA::Frag& pa,
+                                                  const typename SB::Frag& pb, Acc& acc) {
+    const uint32_t la = lds, lb = lds + SA::bytes, fm = wm * MF, fn = wn * NF;
+    if constexpr (PAIR) {
+      u32x4 bh[NF], bl[NF];
 #pragma unroll
-    for (int l = 0; l < L; ++l) {
-      const int r = (wave * L + l) * 8 + (lane >> 3);
-      const int c = (lane & 7) ^ ((r >> 1) & 7);
-      pad[l] = c >= chunks;
-      off[l] = (uint32_t)min(r, o.rows - 1) * o.ld + 16u * (uint32_t)min(c, chunks - 1);
+      for (int j = 0; j < NF; ++j) {
+        bh[j] = pb.read(lb, fn + j, 0, lane);
+        bl[j] = pb.read(lb, fn + j, 1, lane);
+      }
+#pragma unroll
+      for (int i = 0; i < MF; ++i) {
+        const u32x4 ah = pa.read(la, fm + i, 0, lane), al = pa.read(la, fm + i, 1, lane);
+#pragma unroll
+        for (int j = 0; j < NF; ++j) Mma<T>::mul(al, bh[j], acc[i][j]);
+#pragma unroll
+        for (int j = 0; j < NF; ++j) Mma<T>::mul(ah, bl[j], acc[i][j]);
+#pragma unroll
+        for (int j = 0; j < NF; ++j) Mma<T>::mul(ah, bh[j], acc[i][j]);
+      }
+    } else {
+#pragma unroll
+      for (int kk = 0; kk < 2; ++kk) {
+        u32x4 fa[MF], fb[NF];
+#pragma unroll
+        for (int j = 0; j < NF; ++j) fb[j] = pb.read(lb, fn + j, kk, lane);
+#pragma unroll
+        for (int i = 0; i < MF; ++i) fa[i] = pa.read(la, fm + i, kk, lane);
+#pragma unroll
+        for (int i = 0; i < MF; ++i)
+#pragma unroll
+          for (int j = 0; j < NF; ++j) Mma<T>::mul(fa[i], fb[j], acc[i][j]);
+      }
     }
   }
 
-  static __device__ __forceinline__ void stage(const Operand& a, const Operand& b, const uint32_t (&oa)[LA],
-                                               const uint32_t (&ob)[LB], uint64_t k, uint32_t lds, int wave) {
-#pragma unroll
-    for (int l = 0; l < LA; ++l) load_to_lds(a.base + k, oa[l], lds + (wave * LA + l) * 1024);
-#pragma unroll
-    for (int l = 0; l < LB; ++l) load_to_lds(b.base + k, ob[l], lds + BM * kStepBytes + (wave * LB + l) * 1024);
-  }
-
-  static __device__ __forceinline__ void multiply(uint32_t lds, int wm, int wn, int lane, Acc& acc) {
-    const int r = lane & 15, g = lane >> 4;
-    const uint32_t pa = lds + (wm * WM + r) * kStepBytes;
-    const uint32_t pb = lds + BM * kStepBytes + (wn * WN + r) * kStepBytes;
-#pragma unroll
-    for (int kk = 0; kk < 2; ++kk) {
-      const int c = ((kk * 4 + g) ^ ((r >> 1) & 7)) * 16;
-      u32x4 fa[MF], fb[NF];
-#pragma unroll
-      for (int j = 0; j < NF; ++j) fb[j] = lds_read(pb + j * 16 * kStepBytes + c);
-#pragma unroll
-      for (int i = 0; i < MF; ++i) fa[i] = lds_read(pa + i * 16 * kStepBytes + c);
-#pragma unroll
-      for (int i = 0; i < MF; ++i)
-#pragma unroll
-        for (int j = 0; j < NF; ++j) Mma<T>::mul(fa[i], fb[j], acc[i][j]);
-    }
-  }
-
-  // Adds A * B^T over `kbytes` bytes of k (a multiple of 16, > 0) to acc.
-  // On return every wave may still be reading `lds`.
-  static __device__ __forceinline__ void run(const Operand& a, const Operand& b, uint64_t kbytes, uint32_t lds, Acc& acc) {
+  // Adds the product over `k` (> 0) to acc.  On return every wave may still be
+  // reading `lds`.
+  static __device__ __forceinline__ void run(Operand a, Operand b, uint32_t k, uint32_t lds, Acc& acc) {
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int wm = wave / WGN, wn = wave % WGN;
-    const uint32_t steps = (uint32_t)((kbytes + kStepBytes - 1) / kStepBytes);
-    const int last = (int)((kbytes - (uint64_t)(steps - 1) * kStepBytes) / 16);   // chunks of the last step
-    uint32_t oa[LA], ob[LB], ta[LA], tb[LB];
-    bool pa[LA], pb[LB];
-    offsets<LA>(a, wave, lane, 8, oa, pa);
-    offsets<LB>(b, wave, lane, 8, ob, pb);
-    offsets<LA>(a, wave, lane, last, ta, pa);
-    offsets<LB>(b, wave, lane, last, tb, pb);
+    const uint32_t steps = (k + kstep - 1) / kstep;
+    const int left = (int)(k - (steps - 1) * kstep);        // k of the last step
+    const typename SA::Frag pa(lane);
+    const typename SB::Frag pb(lane);
+    uint32_t oa[SA::loads], ob[SB::loads];
+#pragma unroll
+    for (int l = 0; l < SA::loads; ++l) SA::place(a, wave, lane, l, kstep, oa[l]);
+#pragma unroll
+    for (int l = 0; l < SB::loads; ++l) SB::place(b, wave, lane, l, kstep, ob[l]);
+    const uint64_t da = SA::advance(a), db = SB::advance(b);
     auto fetch = [&](uint32_t s) {
-      const uint32_t to = lds + (s & 1) * stage_bytes;
-      if (s + 1 < steps || last == 8) stage(a, b, oa, ob, (uint64_t)s * kStepBytes, to, wave);
-      else stage(a, b, ta, tb, (uint64_t)s * kStepBytes, to, wave);
+      const uint32_t to = lds + (s & 1) * stage_bytes + wave * (SA::loads * 1024);
+      const uint32_t tob = lds + (s & 1) * stage_bytes + SA::bytes + wave * (SB::loads * 1024);
+      const bool whole = s + 1 < steps || left == kstep;
+#pragma unroll
+      for (int l = 0; l < SA::loads; ++l) {
+        uint32_t off = oa[l];
+        if (!whole) SA::place(a, wave, lane, l, left, off);
+        load_to_lds(a.base, off, to + l * 1024);
+      }
+#pragma unroll
+      for (int l = 0; l < SB::loads; ++l) {
+        uint32_t off = ob[l];
+        if (!whole) SB::place(b, wave, lane, l, left, off);
+        load_to_lds(b.base, off, tob + l * 1024);
+      }
+      a.base += da;
+      b.base += db;
     };
     fetch(0);
     for (uint32_t s = 0; s < steps; ++s) {
@@ -157,17 +275,19 @@ struct TileMma {
       const uint32_t at = lds + (s & 1) * stage_bytes;
       if (s + 1 < steps) {
         fetch(s + 1);
-      } else if (last != 8) {
+      } else if (left != kstep) {
         const u32x4 zero = {0, 0, 0, 0};
+        uint32_t unused;
 #pragma unroll
-        for (int l = 0; l < LA; ++l)
-          if (pa[l]) lds_write(at + (wave * LA + l) * 1024 + lane * 16, zero);
+        for (int l = 0; l < SA::loads; ++l)
+          if (SA::place(a, wave, lane, l, left, unused)) lds_write(at + (wave * SA::loads + l) * 1024 + lane * 16, zero);
 #pragma unroll
-        for (int l = 0; l < LB; ++l)
-          if (pb[l]) lds_write(at + BM * kStepBytes + (wave * LB + l) * 1024 + lane * 16, zero);
+        for (int l = 0; l < SB::loads; ++l)
+          if (SB::place(b, wave, lane, l, left, unused))
+            lds_write(at + SA::bytes + (wave * SB::loads + l) * 1024 + lane * 16, zero);
         __syncthreads();
       }
-      multiply(at, wm, wn, lane, acc);
+      multiply(at, wm, wn, lane, pa, pb, acc);
     }
   }
 };

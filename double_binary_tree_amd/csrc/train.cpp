@@ -137,6 +137,7 @@ int ortho_sizes(int nranks, size_t rows, size_t cols, int dtype, OrthoArgs* a) {
   a->rows = (uint32_t)rows;
   a->cols = (uint32_t)cols;
   a->type = static_cast<DType>(dtype);
+  a->cus = current_cus();
   return EMU_SUCCESS;
 }
 
@@ -254,7 +255,6 @@ int emu_orthogonalize(int nranks, const void* const sendbufs[], void* const recv
   }
   spans.out(workspace, need);
   if (spans.clash()) return EMU_ERR_INVALID_ARGUMENT;
-  a.cus = current_cus();
   return orthogonalize(a, static_cast<char*>(workspace), stream) == hipSuccess ? EMU_SUCCESS : EMU_ERR_HIP;
 }
 

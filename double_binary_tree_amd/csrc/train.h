@@ -47,12 +47,11 @@ struct XentLossSpace {
 };
 struct XentGradSpace {
   size_t scale = 0;             // factor on the stored gradients, and its inverse
-  size_t xt = 0;                // x transposed [dim][tpitch]
-  size_t wt = 0;                // the run's rows transposed [dim][vpitch]
-  size_t g = 0, gt = 0;         // d loss / d logits of the run [tokens][vpitch] and transposed [width][tpitch]
+  size_t x = 0;                 // x with zeros for tokens without a loss
+  size_t g = 0;                 // d loss / d logits of the run [tokens][vpitch]
   size_t part = 0;              // [splits][tokens][dim] f32 parts of dx
   size_t bytes = 0;
-  uint32_t tpitch = 0, vpitch = 0;   // in elements
+  uint32_t vpitch = 0;          // in elements
   uint32_t width = 0;           // positions per run, at most
   uint32_t splits = 1;
 };

@@ -10,8 +10,8 @@
 // (m, s) + (m', s') = (M, s exp(m - M) + s' exp(m' - M)), M = max(m, m').
 //
 // The gradient takes the vocabulary in runs: the product is formed again, its
-// epilogue writes g of the run in the inputs' type (token-major and
-// transposed), and two more products read it.  dx is summed in f32 over the
+// epilogue writes g of the run in the inputs' type, and two more products read
+// it: dx along its rows, dw along its columns.  dx is summed in f32 over the
 // runs and rounded once.
 //
 // Vocabulary rows are the product's first operand (lanes hold 4 consecutive
@@ -79,7 +79,7 @@ __global__ __launch_bounds__(K::threads) void xent_stats(Shards sh, LossTile p) 
   const Operand a{static_cast<const char*>(sh.w[r]) + (uint64_t)(sh.row0[r] + row) * ld, ld, rows};
   const Operand b{static_cast<const char*>(p.x) + (uint64_t)tok * ld, ld, (int)(p.tokens - tok)};
   typename K::Acc acc = {};
-  K::run(a, b, ld, lds_address(lds), acc);
+  K::run(a, b, p.dim, lds_address(lds), acc);
 
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, wm = wave / K::WGN, wn = wave % K::WGN;
   __syncthreads();
@@ -177,28 +177,17 @@ __global__ __launch_bounds__(1024) void xent_scale(const float* __restrict__ dlo
   }
 }
 
-// out[c][first + r] = in[r][c], r < rows, and zeros up to the next multiple of
-// kShardAlign; grid: x row tiles of every rank, y column tiles.  With
-// `targets`, rows without a target in [0, vocab) become zeros: a token without
-// a loss then adds nothing to dw, whatever its hidden state holds.
-template <class E>
-__global__ __launch_bounds__(256) void transpose_rows(Shards sh, E* __restrict__ out, uint32_t dim, uint32_t pitch,
-                                                      const int64_t* __restrict__ targets, int64_t vocab) {
-  constexpr int B = 64;
-  __shared__ E tile[B][B + 4 / sizeof(E)];
-  uint32_t m = blockIdx.x;
-  const uint32_t r = rank_of_tile(sh, B, m);
-  const E* in = static_cast<const E*>(sh.w[r]) + (uint64_t)sh.row0[r] * dim;
-  const uint32_t rows = sh.rows[r], pad = (rows + kShardAlign - 1) / kShardAlign * kShardAlign;
-  const uint32_t r0 = m * B, c0 = blockIdx.y * B, x = threadIdx.x % B, y = threadIdx.x / B;
-  for (uint32_t i = y; i < B; i += 4) {
-    bool take = r0 + i < rows && c0 + x < dim;
-    if (take && targets) take = targets[r0 + i] >= 0 && targets[r0 + i] < vocab;
-    tile[i][x] = take ? in[(uint64_t)(r0 + i) * dim + c0 + x] : (E)0.0f;
+// x with zeros in the rows of tokens without a loss: such a token then adds
+// nothing to dw, whatever its hidden state holds.
+__global__ __launch_bounds__(256) void xent_clean(const u32x4* __restrict__ x, const int64_t* __restrict__ targets,
+                                                  uint64_t vecs, uint32_t per_token, int64_t vocab,
+                                                  u32x4* __restrict__ out) {
+  for (uint64_t i = (uint64_t)blockIdx.x * 256 + threadIdx.x; i < vecs; i += (uint64_t)gridDim.x * 256) {
+    const int64_t y = targets[i / per_token];
+    u32x4 v = {0, 0, 0, 0};
+    if (y >= 0 && y < vocab) v = x[i];
+    out[i] = v;
   }
-  __syncthreads();
-  for (uint32_t i = y; i < B; i += 4)
-    if (c0 + i < dim && r0 + x < pad) out[(uint64_t)(c0 + i) * pitch + sh.first[r] + r0 + x] = tile[x][i];
 }
 
 struct GradTile {
@@ -208,14 +197,13 @@ struct GradTile {
   const float* dloss;
   const float* scale;          // null: 1
   void* g;
-  void* gt;                    // null: not wanted
-  uint32_t tokens, dim, vpitch, tpitch, tm, tn, band;
+  uint32_t tokens, dim, vpitch, tm, tn, band;
   int64_t vocab;
 };
 
 // g of the run's rows for every token.  Positions between a rank's last row
-// and the next multiple of kShardAlign, and transposed columns past the last
-// token, become zeros: the products that read g go over whole vectors.
+// and the next multiple of kShardAlign become zeros: the products that read g
+// go over whole vectors.
 template <DType T, class K>
 __global__ __launch_bounds__(K::threads) void xent_dlogits(Shards sh, GradTile p) {
   __shared__ __attribute__((aligned(16))) char lds[K::lds_bytes];
@@ -231,18 +219,17 @@ __global__ __launch_bounds__(K::threads) void xent_dlogits(Shards sh, GradTile p
   const Operand a{static_cast<const char*>(sh.w[r]) + (uint64_t)(sh.row0[r] + row) * ld, ld, rows};
   const Operand b{static_cast<const char*>(p.x) + (uint64_t)tok * ld, ld, (int)(p.tokens - tok)};
   typename K::Acc acc = {};
-  K::run(a, b, ld, lds_address(lds), acc);
+  K::run(a, b, p.dim, lds_address(lds), acc);
 
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, wm = wave / K::WGN, wn = wave % K::WGN;
   const float scale = p.scale ? p.scale[0] : 1.0f;
   const uint32_t first = sh.first[r] + row;
   E* g = static_cast<E*>(p.g);
-  E* gt = static_cast<E*>(p.gt);
 #pragma unroll
   for (int j = 0; j < K::NF; ++j) {
     const uint32_t t = tok + wn * K::WN + j * 16 + (lane & 15), tt = min(t, p.tokens - 1);
     const int64_t id = p.targets[tt];
-    const bool counted = id >= 0 && id < p.vocab && t < p.tokens;
+    const bool counted = id >= 0 && id < p.vocab;
     const int64_t at = id - (int64_t)sh.id0[r] - row;
     const int y = at >= 0 && at < rows ? (int)at : -1;
     const float lse = p.lse[tt], d = p.dloss[tt] * scale;
@@ -255,42 +242,41 @@ __global__ __launch_bounds__(K::threads) void xent_dlogits(Shards sh, GradTile p
         const float q = exp_of(acc[i][j][e] - lse) - (v + e == y ? 1.0f : 0.0f);
         out[e] = (E)(counted && v + e < rows ? d * q : 0.0f);
       }
-      if (v >= padded) continue;
-      if (g && t < p.tokens) *reinterpret_cast<E4*>(g + (uint64_t)t * p.vpitch + first + v) = out;
-      if (gt && t < p.tpitch) {
-#pragma unroll
-        for (int e = 0; e < 4; ++e) gt[(uint64_t)(first + v + e) * p.tpitch + t] = out[e];
-      }
+      if (v < padded && t < p.tokens) *reinterpret_cast<E4*>(g + (uint64_t)t * p.vpitch + first + v) = out;
     }
   }
 }
 
-// dx: first operand the run's rows transposed [dim][width], second g
-// [tokens][width]; workgroup z of gridDim.y sums a share of the width into
-// part[z].
+// dx: first operand the run's rows as they lie in memory (columns of k), second
+// g [tokens][vpitch]; the sum over the run goes rank by rank, and workgroup y
+// of gridDim.y sums a share of its positions into part[y].
 struct DxTile {
-  const void* wt;
   const void* g;
   float* part;
-  uint32_t tokens, dim, width, vpitch, share, tm, tn, band;
+  uint32_t tokens, dim, vpitch, share, tm, tn, band;
   bool add;
 };
 template <DType T, class K>
-__global__ __launch_bounds__(K::threads) void xent_dx(DxTile p) {
+__global__ __launch_bounds__(K::threads) void xent_dx(Shards sh, DxTile p) {
   __shared__ __attribute__((aligned(16))) char lds[K::lds_bytes];
   constexpr int ES = sizeof(typename Elem<T>::type);
   uint32_t m, n;
   tile_of(blockIdx.x, p.tm, p.tn, p.band, m, n);
-  const uint32_t k0 = blockIdx.y * p.share, k1 = min(k0 + p.share, p.width);
-  const uint32_t row = m * K::BM, tok = n * K::BN, ld = p.vpitch * ES;
+  const uint32_t k0 = blockIdx.y * p.share, k1 = k0 + p.share;
+  const uint32_t col = m * K::BM, tok = n * K::BN, wld = p.dim * ES, gld = p.vpitch * ES;
   typename K::Acc acc = {};
-  if (k0 < k1) {
-    const Operand a{static_cast<const char*>(p.wt) + (uint64_t)row * ld + (uint64_t)k0 * ES, ld, (int)(p.dim - row)};
-    const Operand b{static_cast<const char*>(p.g) + (uint64_t)tok * ld + (uint64_t)k0 * ES, ld, (int)(p.tokens - tok)};
-    K::run(a, b, (uint64_t)(k1 - k0) * ES, lds_address(lds), acc);
-  } else if (p.add) {
-    return;
+  bool any = false;
+  for (uint32_t r = 0; r < sh.nranks; ++r) {
+    const uint32_t from = max(k0, sh.first[r]), to = min(k1, sh.first[r] + sh.rows[r]);
+    if (from >= to) continue;
+    if (any) __syncthreads();            // every wave is done with the rank before
+    any = true;
+    const Operand a{static_cast<const char*>(sh.w[r]) + (uint64_t)(sh.row0[r] + from - sh.first[r]) * wld + (uint64_t)col * ES,
+                    wld, (int)(p.dim - col)};
+    const Operand b{static_cast<const char*>(p.g) + (uint64_t)tok * gld + (uint64_t)from * ES, gld, (int)(p.tokens - tok)};
+    K::run(a, b, to - from, lds_address(lds), acc);
   }
+  if (p.add && !any) return;
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, wm = wave / K::WGN, wn = wave % K::WGN;
   float* part = p.part + (uint64_t)blockIdx.y * p.tokens * p.dim;
 #pragma unroll
@@ -298,7 +284,7 @@ __global__ __launch_bounds__(K::threads) void xent_dx(DxTile p) {
     const uint32_t t = tok + wn * K::WN + j * 16 + (lane & 15);
 #pragma unroll
     for (int i = 0; i < K::MF; ++i) {
-      const uint32_t d = row + wm * K::WM + i * 16 + 4 * (lane >> 4);
+      const uint32_t d = col + wm * K::WM + i * 16 + 4 * (lane >> 4);
       if (t >= p.tokens || d >= p.dim) continue;
       f32x4* at = reinterpret_cast<f32x4*>(part + (uint64_t)t * p.dim + d);
       *at = p.add ? *at + acc[i][j] : acc[i][j];
@@ -335,13 +321,13 @@ __global__ __launch_bounds__(256) void xent_zero(Shards sh, uint64_t row_bytes) 
     static_cast<u32x4*>(sh.dw[blockIdx.y])[i] = u32x4{0, 0, 0, 0};
 }
 
-// dw: first operand x transposed [dim][tpitch], second g transposed
-// [width][tpitch].
+// dw: both operands as columns of k (tokens): x [tokens][dim] and g [tokens]
+// [vpitch].
 struct DwTile {
-  const void* xt;
-  const void* gt;
+  const void* x;
+  const void* g;
   const float* scale;
-  uint32_t dim, tpitch, tm, tn, band;
+  uint32_t tokens, dim, vpitch, tm, tn, band;
 };
 template <DType T, class K>
 __global__ __launch_bounds__(K::threads) void xent_dw(Shards sh, DwTile p) {
@@ -351,11 +337,11 @@ __global__ __launch_bounds__(K::threads) void xent_dw(Shards sh, DwTile p) {
   constexpr int ES = sizeof(E);
   uint32_t m, n;
   tile_of(blockIdx.x, p.tm, p.tn, p.band, m, n);
-  const uint32_t r = rank_of_tile(sh, K::BN, n), ld = p.tpitch * ES, col = m * K::BM, row = n * K::BN;
-  const Operand a{static_cast<const char*>(p.xt) + (uint64_t)col * ld, ld, (int)(p.dim - col)};
-  const Operand b{static_cast<const char*>(p.gt) + (uint64_t)(sh.first[r] + row) * ld, ld, (int)(sh.rows[r] - row)};
+  const uint32_t r = rank_of_tile(sh, K::BN, n), col = m * K::BM, row = n * K::BN;
+  const Operand a{static_cast<const char*>(p.x) + (uint64_t)col * ES, p.dim * ES, (int)(p.dim - col)};
+  const Operand b{static_cast<const char*>(p.g) + (uint64_t)(sh.first[r] + row) * ES, p.vpitch * ES, (int)(sh.rows[r] - row)};
   typename K::Acc acc = {};
-  K::run(a, b, ld, lds_address(lds), acc);
+  K::run(a, b, p.tokens, lds_address(lds), acc);
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, wm = wave / K::WGN, wn = wave % K::WGN;
   const float f = p.scale ? p.scale[1] : 1.0f;
   E* dw = static_cast<E*>(sh.dw[r]) + (uint64_t)sh.row0[r] * p.dim;
@@ -376,20 +362,21 @@ __global__ __launch_bounds__(K::threads) void xent_dw(Shards sh, DwTile p) {
 
 // --- tile shapes -------------------------------------------------------------
 
-template <DType T>
-using Big = TileMma<T, 256, 256, 2, 4>;
-template <DType T>
-using Mid = TileMma<T, 128, 128, 2, 2>;
-template <DType T>
-using Thin = TileMma<T, 128, 64, 4, 1>;
+template <DType T, OperandKind A = kRows, OperandKind B = kRows>
+using Big = TileMma<T, 256, 256, 2, 4, A, B>;
+template <DType T, OperandKind A = kRows, OperandKind B = kRows>
+using Mid = TileMma<T, 128, 128, 2, 2, A, B>;
+template <DType T, OperandKind A = kRows, OperandKind B = kRows>
+using Thin = TileMma<T, 128, 64, 4, 1, A, B>;
 
 uint32_t ceil_div(uint32_t a, uint32_t b) { return (a + b - 1) / b; }
 
-// Large tiles once they fill every CU, else the small ones.
+// Large tiles once they fill every CU, else the small ones; never more than
+// twice the width of the second operand (the tokens).
 enum Shape { kBig, kMid, kThin };
 Shape shape_of(uint64_t big_tiles, uint32_t second, int cus) {
-  if (big_tiles >= (uint64_t)cus) return kBig;
-  return second <= 64 ? kThin : kMid;
+  if (second <= 64) return kThin;
+  return second > 128 && big_tiles >= (uint64_t)cus ? kBig : kMid;
 }
 constexpr uint32_t kBmOf[] = {256, 128, 128};
 
@@ -456,17 +443,17 @@ Shards next_run(const Shards& all, uint32_t width, uint64_t& at) {
 template <DType T, class K>
 hipError_t launch_dlogits(const XentArgs& a, const Shards& run, GradTile p, hipStream_t s) {
   p.tm = tiles_of(run, K::BM);
-  p.tn = ceil_div(p.gt ? p.tpitch : p.tokens, K::BN);
+  p.tn = ceil_div(p.tokens, K::BN);
   p.band = 8;
   hipLaunchKernelGGL((xent_dlogits<T, K>), dim3(p.tm * p.tn), dim3(K::threads), 0, s, run, p);
   return hipGetLastError();
 }
 template <DType T, class K>
-hipError_t launch_dx(DxTile p, uint32_t splits, hipStream_t s) {
+hipError_t launch_dx(const Shards& run, DxTile p, uint32_t splits, hipStream_t s) {
   p.tm = ceil_div(p.dim, K::BM);
   p.tn = ceil_div(p.tokens, K::BN);
   p.band = 8;
-  hipLaunchKernelGGL((xent_dx<T, K>), dim3(p.tm * p.tn, splits), dim3(K::threads), 0, s, p);
+  hipLaunchKernelGGL((xent_dx<T, K>), dim3(p.tm * p.tn, splits), dim3(K::threads), 0, s, run, p);
   return hipGetLastError();
 }
 template <DType T, class K>
@@ -484,7 +471,7 @@ Shape dx_shape(const XentArgs& a, uint32_t splits) {
 
 template <DType T>
 hipError_t grad_of(const XentArgs& a, const Shards& all, char* ws, hipStream_t s) {
-  typedef typename Elem<T>::type E;
+  constexpr size_t ES = sizeof(typename Elem<T>::type);
   const bool dx = a.dx != nullptr;
   bool dw = false;
   for (uint32_t r = 0; r < all.nranks; ++r) dw = dw || all.dw[r] != nullptr;
@@ -499,12 +486,10 @@ hipError_t grad_of(const XentArgs& a, const Shards& all, char* ws, hipStream_t s
     scale = reinterpret_cast<const float*>(ws + m.scale);
   }
   if (dw) {
-    Shards xs{};
-    xs.w[0] = a.x;
-    xs.rows[0] = a.tokens;
-    xs.nranks = 1;
-    hipLaunchKernelGGL(transpose_rows<E>, dim3(ceil_div(a.tokens, 64), ceil_div(a.dim, 64)), dim3(256), 0, s, xs,
-                       reinterpret_cast<E*>(ws + m.xt), a.dim, m.tpitch, a.targets, vocab);
+    const uint64_t vecs = (uint64_t)a.tokens * a.dim * ES / kVecBytes;
+    hipLaunchKernelGGL(xent_clean, dim3((uint32_t)std::min<uint64_t>((vecs + 255) / 256, (uint64_t)a.cus * 16)), dim3(256),
+                       0, s, static_cast<const u32x4*>(a.x), a.targets, vecs, (uint32_t)(a.dim * ES / kVecBytes), vocab,
+                       reinterpret_cast<u32x4*>(ws + m.x));
   }
   GradTile gp{};
   gp.x = a.x;
@@ -512,12 +497,10 @@ hipError_t grad_of(const XentArgs& a, const Shards& all, char* ws, hipStream_t s
   gp.lse = a.lse;
   gp.dloss = a.dloss;
   gp.scale = scale;
-  gp.g = dx ? ws + m.g : nullptr;
-  gp.gt = dw ? ws + m.gt : nullptr;
+  gp.g = ws + m.g;
   gp.tokens = a.tokens;
   gp.dim = a.dim;
   gp.vpitch = m.vpitch;
-  gp.tpitch = m.tpitch;
   gp.vocab = vocab;
   uint64_t at = 0;
   bool add = false;
@@ -530,35 +513,32 @@ hipError_t grad_of(const XentArgs& a, const Shards& all, char* ws, hipStream_t s
     }
     if (e) return e;
     if (dx) {
-      hipLaunchKernelGGL(transpose_rows<E>, dim3(tiles_of(run, 64), ceil_div(a.dim, 64)), dim3(256), 0, s, run,
-                         reinterpret_cast<E*>(ws + m.wt), a.dim, m.vpitch, nullptr, vocab);
       DxTile p{};
-      p.wt = ws + m.wt;
       p.g = ws + m.g;
       p.part = reinterpret_cast<float*>(ws + m.part);
       p.tokens = a.tokens;
       p.dim = a.dim;
-      p.width = run.width;
       p.vpitch = m.vpitch;
       p.share = (uint32_t)align_up(ceil_div(run.width, m.splits), 64);
       p.add = add;
       add = true;
       switch (dx_shape(a, m.splits)) {
-        case kBig: e = launch_dx<T, Big<T>>(p, m.splits, s); break;
-        case kMid: e = launch_dx<T, Mid<T>>(p, m.splits, s); break;
-        default: e = launch_dx<T, Thin<T>>(p, m.splits, s); break;
+        case kBig: e = launch_dx<T, Big<T, kCols, kRows>>(run, p, m.splits, s); break;
+        case kMid: e = launch_dx<T, Mid<T, kCols, kRows>>(run, p, m.splits, s); break;
+        default: e = launch_dx<T, Thin<T, kCols, kRows>>(run, p, m.splits, s); break;
       }
       if (e) return e;
     }
     if (dw) {
       DwTile p{};
-      p.xt = ws + m.xt;
-      p.gt = ws + m.gt;
+      p.x = ws + m.x;
+      p.g = ws + m.g;
       p.scale = scale;
+      p.tokens = a.tokens;
       p.dim = a.dim;
-      p.tpitch = m.tpitch;
-      if ((uint64_t)ceil_div(a.dim, 256) * tiles_of(run, 256) >= (uint64_t)a.cus) e = launch_dw<T, Big<T>>(run, p, s);
-      else e = launch_dw<T, Mid<T>>(run, p, s);
+      p.vpitch = m.vpitch;
+      if ((uint64_t)ceil_div(a.dim, 256) * tiles_of(run, 256) >= (uint64_t)a.cus) e = launch_dw<T, Big<T, kCols, kCols>>(run, p, s);
+      else e = launch_dw<T, Mid<T, kCols, kCols>>(run, p, s);
       if (e) return e;
     }
   }
@@ -582,8 +562,7 @@ XentLossSpace xent_loss_space(const XentArgs& a, const Shards& all) {
   return m;
 }
 
-// A run takes as many positions as keep g (one of its two layouts) within
-// 2^27 values, at least 4096; dx is split over the width of a run until its
+// A run takes as many positions as keep g within 2^27 values, at least 4096; dx is split over the width of a run until its
 // tiles reach two per CU, at most 64 ways.
 XentGradSpace xent_grad_space(const XentArgs& a, const Shards& all, bool dx, bool dw) {
   XentGradSpace m;
@@ -592,21 +571,14 @@ XentGradSpace xent_grad_space(const XentArgs& a, const Shards& all, bool dx, boo
   for (uint32_t r = 0; r < all.nranks; ++r) positions += align_up(all.rows[r], kShardAlign);
   m.width = (uint32_t)std::min<uint64_t>(positions, std::max<uint64_t>(4096, (((uint64_t)1 << 27) / a.tokens) / 256 * 256));
   m.vpitch = (uint32_t)align_up(m.width, 64);
-  m.tpitch = (uint32_t)align_up(a.tokens, kShardAlign);
   const uint64_t tiles = (uint64_t)ceil_div(a.dim, 128) * ceil_div(a.tokens, 128);
   while (m.splits < 64 && tiles * m.splits < 2 * (uint64_t)a.cus && m.width / (2 * m.splits) >= 256) m.splits *= 2;
   size_t at = 0;
   auto take = [&](size_t n) { const size_t p = at; at = align_up(at + n, 256); return p; };
   m.scale = take(2 * sizeof(float));
-  if (dw) {
-    m.xt = take((size_t)a.dim * m.tpitch * es);
-    m.gt = take((size_t)m.width * m.tpitch * es);
-  }
-  if (dx) {
-    m.wt = take((size_t)a.dim * m.vpitch * es);
-    m.g = take((size_t)a.tokens * m.vpitch * es);
-    m.part = take((size_t)m.splits * a.tokens * a.dim * sizeof(float));
-  }
+  m.g = take((size_t)a.tokens * m.vpitch * es);
+  if (dw) m.x = take((size_t)a.tokens * a.dim * es);
+  if (dx) m.part = take((size_t)m.splits * a.tokens * a.dim * sizeof(float));
   m.bytes = at;
   return m;
 }
