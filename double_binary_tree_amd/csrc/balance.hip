@@ -5,11 +5,15 @@
 // N the counted tokens of all ranks (those with at least one chosen expert).
 //
 // Three launches.  balance_rows reads every logit once: a group of lanes
-// holds a row in registers, adds its probabilities to the group's own column
-// sums and its choices to the workgroup's integer counts, and leaves one row
-// of partial sums per workgroup.  balance_join adds those rows in ascending
-// order (so results repeat bit for bit) in 64 bits and forms f.
-// balance_grad reads the logits again and writes their gradients.
+// holds rows in registers, adds their probabilities to the group's own column
+// sums and their choices to the workgroup's integer counts, and leaves one row
+// of partial sums per workgroup.  balance_join adds those rows in 64 bits, in
+// an order that the sizes fix, and forms f.  balance_grad reads the logits
+// again and writes their gradients; its first workgroup (without gradients:
+// balance_total) adds up the loss.  (Joining rank by rank in separate
+// workgroups, the last of which adds the ranks, took 17 us for 8 ranks x 128
+// partial rows x 256 experts: a release to the other XCDs writes back a whole
+// L2.  One workgroup for all ranks of 16 experts takes 10 us.)
 #include "device_ops.h"
 #include "train.h"
 
@@ -28,6 +32,31 @@ template <>
 struct Elem<DType::F16> { typedef _Float16 type; };
 template <>
 struct Elem<DType::BF16> { typedef __bf16 type; };
+
+// Reductions over the lanes of a group (a power of two, the same for every
+// lane); every lane gets the result.  Within 16 lanes data moves through DPP
+// operands: after the exchanges with lanes xor 1 and xor 2 a quad holds one
+// value, so mirroring 8 (then 16) lanes brings the other quad's (half's).
+template <int CTRL>
+__device__ __forceinline__ float dpp(float x) {
+  return bits<float>(__builtin_amdgcn_mov_dpp(bits<int>(x), CTRL, 0xF, 0xF, true));
+}
+template <class F>
+__device__ __forceinline__ float reduce(float x, uint32_t group, F op) {
+  if (group > 1) x = op(x, dpp<0xB1>(x));      // quad_perm 1 0 3 2
+  if (group > 2) x = op(x, dpp<0x4E>(x));      // quad_perm 2 3 0 1
+  if (group > 4) x = op(x, dpp<0x141>(x));     // row_half_mirror
+  if (group > 8) x = op(x, dpp<0x140>(x));     // row_mirror
+  if (group > 16) x = op(x, __shfl_xor(x, 16));
+  if (group > 32) x = op(x, __shfl_xor(x, 32));
+  return x;
+}
+struct Max {
+  __device__ __forceinline__ float operator()(float a, float b) const { return fmaxf(a, b); }
+};
+struct Add {
+  __device__ __forceinline__ float operator()(float a, float b) const { return a + b; }
+};
 
 // One row in a group's registers: lane `l` of `group` lanes holds columns
 // (l + i * group) * VEC + v.  Columns past the row read as -inf.
@@ -80,7 +109,7 @@ struct Row {
     for (int i = 0; i < NI; ++i)
 #pragma unroll
       for (int v = 0; v < VEC; ++v) m = fmaxf(m, z[i][v]);
-    for (uint32_t d = 1; d < group; d <<= 1) m = fmaxf(m, __shfl_xor(m, d));
+    m = reduce(m, group, Max());
     if (m == -INFINITY) m = 0.0f;
     float s = 0.0f;
 #pragma unroll
@@ -90,7 +119,7 @@ struct Row {
         z[i][v] = __builtin_amdgcn_exp2f((z[i][v] - m) * 1.44269504088896341f);
         s += z[i][v];
       }
-    for (uint32_t d = 1; d < group; d <<= 1) s += __shfl_xor(s, d);
+    s = reduce(s, group, Add());
     const float r = s == 0.0f ? 0.0f : 1.0f / s;
 #pragma unroll
     for (int i = 0; i < NI; ++i)
@@ -100,19 +129,29 @@ struct Row {
 };
 
 // Whether token `row` chose any expert, seen by every lane of its group; adds
-// its choices to `counts` (LDS) if given.
-__device__ __forceinline__ bool chosen(const int32_t* experts, uint64_t row, uint32_t topk, uint32_t nexperts,
-                                       uint32_t l, uint32_t group, uint32_t* counts) {
-  int any = 0;
+// its choices to `counts` (LDS) if given.  `first`: the lane's first choice.
+__device__ __forceinline__ bool chosen(const int32_t* experts, uint64_t row, int32_t first, uint32_t topk,
+                                       uint32_t nexperts, uint32_t l, uint32_t group, uint32_t* counts) {
+  bool any = false;
   for (uint32_t k = l; k < topk; k += group) {
-    const uint32_t e = (uint32_t)experts[row * topk + k];
+    const uint32_t e = (uint32_t)(k == l ? first : experts[row * topk + k]);
     if (e < nexperts) {
-      any = 1;
+      any = true;
       if (counts) atomicAdd(&counts[e], 1u);
     }
   }
-  for (uint32_t d = 1; d < group; d <<= 1) any |= __shfl_xor(any, d);
-  return any != 0;
+  const uint64_t lanes = __ballot(any) >> (threadIdx.x & 63 & ~(group - 1));
+  return (group == 64 ? lanes : lanes & (((uint64_t)1 << group) - 1)) != 0;
+}
+
+// Rows that a group loads before it works on the first.
+template <int VEC, int NI>
+constexpr int rows_ahead() {
+  return VEC * NI >= 16 ? 2 : 4;
+}
+// Lane l's first choice of token `row` (-1 past topk).
+__device__ __forceinline__ int32_t first_choice(const int32_t* experts, uint64_t row, uint32_t topk, uint32_t l) {
+  return l < topk ? experts[row * topk + l] : -1;
 }
 
 // Which rank and rows workgroup `b` has: rank r's tokens are split into
@@ -127,10 +166,21 @@ __device__ __forceinline__ uint32_t rank_of(const BalanceGrid& g, uint32_t nrank
   return r;
 }
 
+constexpr int kJoinExperts = 16, kJoinLanes = 64, kJoinThreads = kJoinExperts * kJoinLanes;
+
+// What the launches leave to each other.
+struct BalanceSums {
+  float* psum;             // [workgroup][expert] sums of probabilities
+  uint32_t* pcount;        // [workgroup][expert] choices
+  uint32_t* pvalid;        // [workgroup] rows that take part
+  double* term;            // [expert] f P
+  float* f;                // [expert]
+  float* scale;            // coef E / N
+};
+
 template <DType T, int VEC, int NI>
 __global__ __launch_bounds__(kBalThreads) void balance_rows(BalanceArgs a, BalanceGrid g, uint32_t group,
-                                                          float* __restrict__ psum, uint32_t* __restrict__ pcount,
-                                                          uint32_t* __restrict__ pvalid) {
+                                                          BalanceSums p) {
   extern __shared__ char lds[];
   float* sums = reinterpret_cast<float*>(lds);                     // [kBalWaves][nexperts]
   uint32_t* counts = reinterpret_cast<uint32_t*>(sums + kBalWaves * a.nexperts);
@@ -143,18 +193,28 @@ __global__ __launch_bounds__(kBalThreads) void balance_rows(BalanceArgs a, Balan
   __syncthreads();
   float acc[NI][VEC] = {};
   uint32_t mine = 0;
-  for (uint32_t first = begin; first < end; first += slots) {
-    const uint32_t row = first + slot;
-    if (row >= end) continue;                                      // whole groups
-    if (!chosen(a.experts[r], row, a.topk, a.nexperts, l, group, counts)) continue;
-    Row<T, VEC, NI> z;
-    z.load(a.logits[r], row, a.nexperts, l, group);
-    z.softmax(group);
-    if (l == 0) ++mine;
+  constexpr int R = rows_ahead<VEC, NI>();
+  for (uint32_t row0 = begin + slot; row0 < end; row0 += R * slots) {
+    Row<T, VEC, NI> z[R];
+    int32_t pick[R];
 #pragma unroll
-    for (int i = 0; i < NI; ++i)
+    for (int q = 0; q < R; ++q) {
+      const uint32_t row = min(row0 + q * slots, end - 1);
+      pick[q] = first_choice(a.experts[r], row, a.topk, l);
+      z[q].load(a.logits[r], row, a.nexperts, l, group);
+    }
 #pragma unroll
-      for (int v = 0; v < VEC; ++v) acc[i][v] += z.z[i][v];
+    for (int q = 0; q < R; ++q) {
+      const uint32_t row = row0 + q * slots;
+      if (row >= end) continue;                                    // whole groups
+      if (!chosen(a.experts[r], row, pick[q], a.topk, a.nexperts, l, group, counts)) continue;
+      z[q].softmax(group);
+      if (l == 0) ++mine;
+#pragma unroll
+      for (int i = 0; i < NI; ++i)
+#pragma unroll
+        for (int v = 0; v < VEC; ++v) acc[i][v] += z[q].z[i][v];
+    }
   }
   if (mine) atomicAdd(&nvalid, mine);
   // the groups of a wave hold the same columns: add them, then the waves
@@ -171,73 +231,84 @@ __global__ __launch_bounds__(kBalThreads) void balance_rows(BalanceArgs a, Balan
   for (uint32_t e = threadIdx.x; e < a.nexperts; e += kBalThreads) {
     float s = 0.0f;
     for (int w = 0; w < kBalWaves; ++w) s += sums[w * a.nexperts + e];
-    psum[(uint64_t)b * a.nexperts + e] = s;
-    pcount[(uint64_t)b * a.nexperts + e] = counts[e];
+    p.psum[(uint64_t)b * a.nexperts + e] = s;
+    p.pcount[(uint64_t)b * a.nexperts + e] = counts[e];
   }
-  if (threadIdx.x == 0) pvalid[b] = nvalid;
+  if (threadIdx.x == 0) p.pvalid[b] = nvalid;
 }
 
-// One workgroup per 16 experts, 16 lanes each: lane k of an expert adds the
-// partial rows k, k + 16, ... of a rank, and the 16 parts are added in order.
-constexpr int kJoinExperts = 16, kJoinLanes = 16;
-__global__ __launch_bounds__(kJoinExperts* kJoinLanes) void balance_join(BalanceArgs a, BalanceGrid g,
-                                                                         const float* __restrict__ psum,
-                                                                         const uint32_t* __restrict__ pcount,
-                                                                         const uint32_t* __restrict__ pvalid,
-                                                                         float* __restrict__ f,
-                                                                         double* __restrict__ term,
-                                                                         float* __restrict__ inv) {
+// 16 experts a workgroup, 64 lanes each: lane k of an expert adds the partial
+// rows k, k + 64, ..., and the 64 parts are added in order.
+__global__ __launch_bounds__(kJoinThreads) void balance_join(BalanceArgs a, BalanceGrid g, BalanceSums p) {
   __shared__ double dsum[kJoinLanes][kJoinExperts];
-  __shared__ unsigned long long csum[kJoinLanes][kJoinExperts];
+  __shared__ unsigned long long csum[kMaxRanks][kJoinExperts], nvalid;
+  __shared__ uint32_t block0[kMaxRanks + 1];
   const uint32_t le = threadIdx.x % kJoinExperts, k = threadIdx.x / kJoinExperts;
-  const uint32_t e = blockIdx.x * kJoinExperts + le;
-  const uint32_t nblocks = g.block0[a.nranks];
-  unsigned long long n = 0;
-  for (uint32_t b = threadIdx.x; b < nblocks; b += kJoinExperts * kJoinLanes) n += pvalid[b];
-  csum[k][le] = n;
+  const uint32_t e = blockIdx.x * kJoinExperts + le, nblocks = g.block0[a.nranks];
+  csum[k][le] = 0;
+  if (threadIdx.x == 0) nvalid = 0;
+  if (threadIdx.x <= a.nranks) block0[threadIdx.x] = g.block0[threadIdx.x];
   __syncthreads();
-  n = 0;
-  for (int i = 0; i < kJoinLanes; ++i)
-    for (int j = 0; j < kJoinExperts; ++j) n += csum[i][j];
+  unsigned long long n = 0;
+  for (uint32_t b = threadIdx.x; b < nblocks; b += kJoinThreads) n += p.pvalid[b];
+  if (n) atomicAdd(&nvalid, n);
   double s = 0.0;
-  unsigned long long total = 0;
-  for (uint32_t r = 0; r < a.nranks; ++r) {
-    unsigned long long c = 0;
-    if (e < a.nexperts)
-      for (uint32_t b = g.block0[r] + k; b < g.block0[r + 1]; b += kJoinLanes) {
-        s += (double)psum[(uint64_t)b * a.nexperts + e];
-        c += pcount[(uint64_t)b * a.nexperts + e];
+  if (e < a.nexperts) {
+    uint32_t r = 0;
+    constexpr uint32_t kBatch = 8;
+    for (uint32_t b = k; b < nblocks; b += kBatch * kJoinLanes) {
+      float x[kBatch];
+      uint32_t c[kBatch];
+#pragma unroll
+      for (uint32_t i = 0; i < kBatch; ++i) {
+        const uint64_t at = (uint64_t)min(b + i * kJoinLanes, nblocks - 1) * a.nexperts + e;
+        x[i] = p.psum[at];
+        c[i] = p.pcount[at];
       }
-    __syncthreads();
-    csum[k][le] = c;
-    __syncthreads();
-    if (k == 0 && e < a.nexperts) {
-      c = 0;
-      for (int i = 0; i < kJoinLanes; ++i) c += csum[i][le];
-      a.counts[(uint64_t)r * a.nexperts + e] = (int64_t)c;
-      total += c;
+#pragma unroll
+      for (uint32_t i = 0; i < kBatch; ++i) {
+        if (b + i * kJoinLanes >= nblocks) break;
+        while (b + i * kJoinLanes >= block0[r + 1]) ++r;
+        s += (double)x[i];
+        atomicAdd(&csum[r][le], (unsigned long long)c[i]);
+      }
     }
   }
   dsum[k][le] = s;
   __syncthreads();
-  if (k == 0 && e < a.nexperts) {
+  if (e >= a.nexperts) return;
+  if (k < a.nranks) a.counts[(uint64_t)k * a.nexperts + e] = (int64_t)csum[k][le];
+  if (k == 0) {
+    unsigned long long c = 0;
     s = 0.0;
+    for (uint32_t r = 0; r < a.nranks; ++r) c += csum[r][le];
     for (int i = 0; i < kJoinLanes; ++i) s += dsum[i][le];
-    a.counts[(uint64_t)a.nranks * a.nexperts + e] = (int64_t)total;
-    const double share = n ? (double)total / ((double)n * a.topk) : 0.0;
-    f[e] = (float)share;
-    term[e] = n ? share * (s / (double)n) : 0.0;
-    if (e == 0) *inv = n ? (float)((double)a.coef * a.nexperts / (double)n) : 0.0f;
+    a.counts[(uint64_t)a.nranks * a.nexperts + e] = (int64_t)c;
+    const double share = nvalid ? (double)c / ((double)nvalid * a.topk) : 0.0;
+    p.f[e] = (float)share;
+    p.term[e] = nvalid ? share * (s / (double)nvalid) : 0.0;
+    if (e == 0) *p.scale = nvalid ? (float)((double)a.coef * a.nexperts / (double)nvalid) : 0.0f;
   }
 }
 
+// The loss, by one wave.
+__device__ __forceinline__ void total(const BalanceArgs& a, const double* term) {
+  double s = 0.0;
+  for (uint32_t e = threadIdx.x; e < a.nexperts; e += 64) s += term[e];
+  for (int d = 1; d < 64; d <<= 1) s += __shfl_xor(s, d);
+  if (threadIdx.x == 0) *a.loss = (float)((double)a.coef * a.nexperts * s);
+}
+__global__ __launch_bounds__(64) void balance_total(BalanceArgs a, const double* __restrict__ term) { total(a, term); }
+
 template <DType T, int VEC, int NI>
 __global__ __launch_bounds__(kBalThreads) void balance_grad(BalanceArgs a, BalanceGrid g, uint32_t group,
-                                                          const float* __restrict__ f, const float* __restrict__ inv) {
+                                                          const float* __restrict__ f, const float* __restrict__ coef,
+                                                          const double* __restrict__ term) {
   const uint32_t b = blockIdx.x, r = rank_of(g, a.nranks, b);
   const uint32_t begin = (b - g.block0[r]) * g.rows, end = min(begin + g.rows, a.tokens[r]);
   const uint32_t l = threadIdx.x & (group - 1), slot = threadIdx.x / group, slots = kBalThreads / group;
-  const float scale = *inv;
+  if (b == 0 && threadIdx.x < 64) total(a, term);
+  const float scale = *coef;
   float fe[NI][VEC];
 #pragma unroll
   for (int i = 0; i < NI; ++i)
@@ -246,88 +317,77 @@ __global__ __launch_bounds__(kBalThreads) void balance_grad(BalanceArgs a, Balan
       const uint32_t c = (l + i * group) * VEC + v;
       fe[i][v] = c < a.nexperts ? f[c] : 0.0f;
     }
-  for (uint32_t first = begin; first < end; first += slots) {
-    const uint32_t row = first + slot;
-    if (row >= end) continue;
-    Row<T, VEC, NI> z;
-    if (chosen(a.experts[r], row, a.topk, a.nexperts, l, group, nullptr)) {
-      z.load(a.logits[r], row, a.nexperts, l, group);
-      z.softmax(group);
+  constexpr int R = rows_ahead<VEC, NI>();
+  for (uint32_t row0 = begin + slot; row0 < end; row0 += R * slots) {
+    Row<T, VEC, NI> z[R];
+    int32_t pick[R];
+#pragma unroll
+    for (int q = 0; q < R; ++q) {
+      const uint32_t row = min(row0 + q * slots, end - 1);
+      pick[q] = first_choice(a.experts[r], row, a.topk, l);
+      z[q].load(a.logits[r], row, a.nexperts, l, group);
+    }
+#pragma unroll
+    for (int q = 0; q < R; ++q) {
+      const uint32_t row = row0 + q * slots;
+      if (row >= end) continue;
+      const bool live = chosen(a.experts[r], row, pick[q], a.topk, a.nexperts, l, group, nullptr);
+      z[q].softmax(group);
       float dot = 0.0f;
 #pragma unroll
       for (int i = 0; i < NI; ++i)
 #pragma unroll
-        for (int v = 0; v < VEC; ++v) dot += fe[i][v] * z.z[i][v];
-      for (uint32_t d = 1; d < group; d <<= 1) dot += __shfl_xor(dot, d);
+        for (int v = 0; v < VEC; ++v) dot += fe[i][v] * z[q].z[i][v];
+      dot = reduce(dot, group, Add());
 #pragma unroll
       for (int i = 0; i < NI; ++i)
 #pragma unroll
-        for (int v = 0; v < VEC; ++v) z.z[i][v] = scale * z.z[i][v] * (fe[i][v] - dot);
-    } else {
-#pragma unroll
-      for (int i = 0; i < NI; ++i)
-#pragma unroll
-        for (int v = 0; v < VEC; ++v) z.z[i][v] = 0.0f;
+        for (int v = 0; v < VEC; ++v) z[q].z[i][v] = live ? scale * z[q].z[i][v] * (fe[i][v] - dot) : 0.0f;
+      z[q].store(a.dlogits[r], row, a.nexperts, l, group);
     }
-    z.store(a.dlogits[r], row, a.nexperts, l, group);
   }
 }
 
-__global__ __launch_bounds__(64) void balance_total(BalanceArgs a, const double* __restrict__ term) {
-  double s = 0.0;
-  for (uint32_t e = threadIdx.x; e < a.nexperts; e += 64) s += term[e];
-  for (int d = 1; d < 64; d <<= 1) s += __shfl_xor(s, d);
-  if (threadIdx.x == 0) *a.loss = (float)((double)a.coef * a.nexperts * s);
-}
-
-// Tokens per workgroup: 32 rows in flight at least, more when that still
-// leaves four workgroups per CU.
+// Tokens per workgroup: what gives four workgroups per CU, in powers of two
+// from 64 to 4096.
 BalanceGrid balance_grid(const BalanceArgs& a) {
   uint64_t all = 0;
   for (uint32_t r = 0; r < a.nranks; ++r) all += a.tokens[r];
   BalanceGrid g{};
   const uint64_t want = (all + 4u * a.cus - 1) / (4u * a.cus);
-  g.rows = 32;
+  g.rows = 64;
   while (g.rows < want && g.rows < 4096) g.rows *= 2;
   for (uint32_t r = 0; r < a.nranks; ++r) g.block0[r + 1] = g.block0[r] + (a.tokens[r] + g.rows - 1) / g.rows;
   return g;
 }
 
-struct BalanceSpace {
-  size_t psum, pcount, pvalid, f, term, inv, bytes;
-};
-BalanceSpace layout(const BalanceArgs& a, uint32_t nblocks) {
-  BalanceSpace s{};
+// The sums in the caller's workspace; returns its size.
+size_t layout(const BalanceArgs& a, uint32_t nblocks, char* ws, BalanceSums* p) {
   size_t at = 0;
-  auto take = [&](size_t n) { const size_t p = at; at = align_up(at + n, 256); return p; };
-  s.psum = take((size_t)nblocks * a.nexperts * 4);
-  s.pcount = take((size_t)nblocks * a.nexperts * 4);
-  s.pvalid = take((size_t)nblocks * 4);
-  s.f = take((size_t)a.nexperts * 4);
-  s.term = take((size_t)a.nexperts * 8);
-  s.inv = take(4);
-  s.bytes = at;
-  return s;
+  auto take = [&](size_t n) { char* o = ws + at; at = align_up(at + n, 256); return o; };
+  const size_t e = a.nexperts;
+  p->psum = reinterpret_cast<float*>(take(nblocks * e * 4));
+  p->pcount = reinterpret_cast<uint32_t*>(take(nblocks * e * 4));
+  p->pvalid = reinterpret_cast<uint32_t*>(take((size_t)nblocks * 4));
+  p->term = reinterpret_cast<double*>(take(e * 8));
+  p->f = reinterpret_cast<float*>(take(e * 4));
+  p->scale = reinterpret_cast<float*>(take(4));
+  return at;
 }
 
 template <DType T, int VEC, int NI>
 hipError_t launch(const BalanceArgs& a, const BalanceGrid& g, uint32_t group, char* ws, hipStream_t s) {
   const uint32_t nblocks = g.block0[a.nranks];
-  const BalanceSpace m = layout(a, nblocks);
-  float* psum = reinterpret_cast<float*>(ws + m.psum);
-  uint32_t* pcount = reinterpret_cast<uint32_t*>(ws + m.pcount);
-  uint32_t* pvalid = reinterpret_cast<uint32_t*>(ws + m.pvalid);
-  float* f = reinterpret_cast<float*>(ws + m.f);
-  double* term = reinterpret_cast<double*>(ws + m.term);
-  float* inv = reinterpret_cast<float*>(ws + m.inv);
+  BalanceSums p;
+  layout(a, nblocks, ws, &p);
   if (nblocks)
-    hipLaunchKernelGGL((balance_rows<T, VEC, NI>), dim3(nblocks), dim3(kBalThreads),
-                       (kBalWaves + 1) * a.nexperts * 4, s, a, g, group, psum, pcount, pvalid);
-  hipLaunchKernelGGL(balance_join, dim3((a.nexperts + kJoinExperts - 1) / kJoinExperts),
-                     dim3(kJoinExperts * kJoinLanes), 0, s, a, g, psum, pcount, pvalid, f, term, inv);
-  hipLaunchKernelGGL(balance_total, dim3(1), dim3(64), 0, s, a, term);
-  if (nblocks && a.grad)
-    hipLaunchKernelGGL((balance_grad<T, VEC, NI>), dim3(nblocks), dim3(kBalThreads), 0, s, a, g, group, f, inv);
+    hipLaunchKernelGGL((balance_rows<T, VEC, NI>), dim3(nblocks), dim3(kBalThreads), (kBalWaves + 1) * a.nexperts * 4, s,
+                       a, g, group, p);
+  hipLaunchKernelGGL(balance_join, dim3((a.nexperts + kJoinExperts - 1) / kJoinExperts), dim3(kJoinThreads), 0, s, a, g, p);
+  if (a.grad && nblocks)
+    hipLaunchKernelGGL((balance_grad<T, VEC, NI>), dim3(nblocks), dim3(kBalThreads), 0, s, a, g, group, p.f, p.scale, p.term);
+  else
+    hipLaunchKernelGGL(balance_total, dim3(1), dim3(64), 0, s, a, p.term);
   return hipGetLastError();
 }
 
@@ -337,8 +397,14 @@ hipError_t dispatch(const BalanceArgs& a, char* ws, hipStream_t s) {
   const BalanceGrid g = balance_grid(a);
   const bool whole = a.nexperts % V == 0;      // every row starts on a vector
   const uint32_t units = whole ? a.nexperts / V : a.nexperts;
+  // Up to 16 values of a row per lane: the exchanges of a row's maximum and
+  // sums are shared by the rows of a wave, so few lanes per row are cheapest.
+  // One vector a lane (64 lanes a row at 256 f32 experts) took 62 + 84 us for
+  // the two passes over 8 x 16384 rows, this
+  // 29 + 44 us (4.7 and 6.1 TB/s).
+  const uint32_t most = whole ? 16 / V : 16;
   uint32_t group = 1;
-  while (group < 64 && group < units) group *= 2;
+  while (group < 64 && group * most < units) group *= 2;
   const uint32_t ni = (units + group - 1) / group;
   if (whole) {
     if (ni == 1) return launch<T, V, 1>(a, g, group, ws, s);
@@ -352,7 +418,10 @@ hipError_t dispatch(const BalanceArgs& a, char* ws, hipStream_t s) {
 
 }  // namespace
 
-size_t balance_space(const BalanceArgs& a) { return layout(a, balance_grid(a).block0[a.nranks]).bytes; }
+size_t balance_space(const BalanceArgs& a) {
+  BalanceSums p;
+  return layout(a, balance_grid(a).block0[a.nranks], nullptr, &p);
+}
 
 int balance_loss(const BalanceArgs& a, char* workspace, void* stream) {
   hipStream_t s = static_cast<hipStream_t>(stream);

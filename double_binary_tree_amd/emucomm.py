@@ -369,11 +369,11 @@ def all_gather_tensors(sends, recvs, stream=None) -> None:
 # streams, two captured graphs) need a workspace each.
 
 def _sizes(values):
-    return (ctypes.c_size_t * max(len(values), 1))(*[int(v) for v in values])
+    return (ctypes.c_size_t * max(len(values), 1))(*values)
 
 
 def _opt_ptrs(ptrs):
-    return None if ptrs is None else _ptrs([0 if p is None else p for p in ptrs])
+    return None if ptrs is None else (ctypes.c_void_p * max(len(ptrs), 1))(*ptrs)
 
 
 def cross_entropy_workspace_raw(vocab, tokens: int, dim: int, dtype: int, want_dx: int, want_dw: int):
@@ -432,7 +432,7 @@ def _float_name(t) -> str:
 
 
 def _expect(t, shape, dtype, device, what: str):
-    if t.dtype != dtype or tuple(t.shape) != tuple(shape) or t.device != device or not t.is_contiguous():
+    if t.dtype is not dtype or t.shape != shape or t.device != device or not t.is_contiguous():
         raise ValueError(f"{what} must be a contiguous {dtype} tensor of shape {tuple(shape)} on {device}, got "
                          f"{t.dtype} {tuple(t.shape)} on {t.device}")
 
