@@ -23,6 +23,8 @@
 // the diagonal are computed, and each is written twice.  Pairs lie as tile.h
 // wants them, in blocks of 32 hi and 32 lo; without pairs the lo part of X
 // has an array of its own, which only the a X term reads.
+#include <type_traits>
+
 #include "tile.h"
 #include "train.h"
 
@@ -156,42 +158,43 @@ __device__ __forceinline__ void triangle(uint32_t t, uint32_t& i, uint32_t& j) {
   i = (uint32_t)((sqrtf(8.0f * (float)t + 1.0f) - 1.0f) * 0.5f);
   while (i * (i + 1) / 2 > t) --i;
   while ((i + 1) * (i + 2) / 2 <= t) ++i;
+  i = uniform(i);
   j = t - i * (i + 1) / 2;
 }
 
 // What a symmetric product does with its tile.  kGram: A = X X^T;
-// kPoly: B = b A + c A A.
+// kPoly: B = b A + c A A, plus a on the diagonal with pairs (X' = (a + B) X
+// then needs no second look at X; without pairs a's product with X would lose
+// X's lo part).
 enum SymKind { kGram, kPoly };
+
 template <class K, bool PAIR, SymKind KIND>
-__global__ __launch_bounds__(K::threads) void ortho_sym(OrthoMat q, char* ws, uint32_t cur, float cb, float cc) {
-  __shared__ __attribute__((aligned(16))) char lds[K::lds_bytes];
-  static_assert(K::BM == K::BN, "square tiles");
-  uint32_t ti, tj;
-  triangle(blockIdx.x, ti, tj);
-  char* base = ws + blockIdx.y * q.bytes;
-  const uint32_t r0 = ti * K::BM, c0 = tj * K::BN;
-  typename K::Acc acc = {};
-  const uint32_t pitch = KIND == kGram ? q.xp : q.ap;
-  const char* src = base + (KIND == kGram ? q.x[cur] : q.a);
-  const Operand a{src + (uint64_t)r0 * pitch, pitch, (int)(q.m - r0)}, b{src + (uint64_t)c0 * pitch, pitch, (int)(q.m - c0)};
-  K::run(a, b, KIND == kGram ? q.n : q.m, lds_address(lds), acc);
+__device__ __forceinline__ void sym_store(const OrthoMat& q, char* base, uint32_t ti, uint32_t tj, float ca, float cb, float cc,
+                                          typename K::Acc& acc) {
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, wm = wave / K::WGN, wn = wave % K::WGN;
   char* out = base + (KIND == kGram ? q.a : q.b);
   const uint32_t width = q.ap / (PAIR ? 4 : 2);
 #pragma unroll
   for (int j = 0; j < K::NF; ++j) {
-    const uint32_t c = c0 + wn * K::WN + j * 16 + (lane & 15);
+    const uint32_t c = tj * K::BN + wn * K::WN + j * 16 + (lane & 15);
+    float old[K::MF][4];
+    if (KIND == kPoly) {                 // all reads before the first store, which could alias them
+#pragma unroll
+      for (int i = 0; i < K::MF; ++i) {
+        const uint32_t r = ti * K::BM + wm * K::WM + i * 16 + 4 * (lane >> 4);
+        get<PAIR>(base + q.a + (uint64_t)min(c, q.m - 1) * q.ap, nullptr, min(r, width - 4), old[i]);
+      }
+    }
 #pragma unroll
     for (int i = 0; i < K::MF; ++i) {
-      const uint32_t r = r0 + wm * K::WM + i * 16 + 4 * (lane >> 4);
+      const uint32_t r = ti * K::BM + wm * K::WM + i * 16 + 4 * (lane >> 4);
       // row c, columns r .. r + 3 (on and above the diagonal), and its mirror
       if (c >= q.m || r >= width) continue;
-      float v[4], old[4];
-      if (KIND == kPoly) get<PAIR>(base + q.a + (uint64_t)c * q.ap, nullptr, r, old);
+      float v[4];
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
         v[e] = acc[i][j][e] * kInvScale;
-        if (KIND == kPoly) v[e] = cb * old[e] + cc * v[e];
+        if (KIND == kPoly) v[e] = cb * old[i][e] + cc * v[e] + (PAIR && r + e == c ? ca * kScale : 0.0f);
         if (r + e >= q.m) v[e] = 0.0f;
       }
       put<PAIR>(out + (uint64_t)c * q.ap, nullptr, r, v);
@@ -210,38 +213,100 @@ __global__ __launch_bounds__(K::threads) void ortho_sym(OrthoMat q, char* ws, ui
   }
 }
 
+// Work items run matrix by matrix, share of k by share (each XCD then reads
+// few matrices), tile by tile.  With several shares each leaves a part, which
+// ortho_sym_join adds.
+template <class K, bool PAIR, SymKind KIND>
+__global__ __launch_bounds__(K::threads) void ortho_sym(OrthoMat q, char* ws, float* parts, uint32_t cur, uint32_t tiles,
+                                                        uint32_t shares, uint32_t share, float ca, float cb, float cc) {
+  __shared__ __attribute__((aligned(16))) char lds[K::lds_bytes];
+  static_assert(K::BM == K::BN, "square tiles");
+  uint32_t ti, tj;
+  const uint32_t item = xcd_share(blockIdx.x, gridDim.x), group = uniform(item / tiles);
+  const uint32_t mat = uniform(group / shares), z = group - mat * shares;
+  triangle(item - group * tiles, ti, tj);
+  char* base = ws + mat * q.bytes;
+  const uint32_t r0 = ti * K::BM, c0 = tj * K::BN;
+  typename K::Acc acc = {};
+  const uint32_t pitch = KIND == kGram ? q.xp : q.ap, k = KIND == kGram ? q.n : q.m;
+  const uint32_t k0 = z * share;                           // a multiple of 32
+  const char* src = base + (KIND == kGram ? q.x[cur] : q.a) + (uint64_t)k0 * (PAIR ? 4 : 2);
+  const Operand a{src + (uint64_t)r0 * pitch, pitch, (int)(q.m - r0)}, b{src + (uint64_t)c0 * pitch, pitch, (int)(q.m - c0)};
+  K::run(a, b, min(k - k0, share), lds_address(lds), acc);
+  if (shares > 1) {
+    f32x4* to = reinterpret_cast<f32x4*>(parts) + (uint64_t)item * (K::BM * K::BN / 4) + threadIdx.x;
+#pragma unroll
+    for (int i = 0; i < K::MF; ++i)
+#pragma unroll
+      for (int j = 0; j < K::NF; ++j) to[(i * K::NF + j) * K::threads] = acc[i][j];
+    return;
+  }
+  sym_store<K, PAIR, KIND>(q, base, ti, tj, ca, cb, cc, acc);
+}
+
+// The parts of a tile added in order, then as in ortho_sym.
+template <class K, bool PAIR, SymKind KIND>
+__global__ __launch_bounds__(K::threads) void ortho_sym_join(OrthoMat q, char* ws, const float* __restrict__ parts,
+                                                             uint32_t nparts, float ca, float cb, float cc) {
+  uint32_t ti, tj;
+  triangle(blockIdx.x, ti, tj);
+  typename K::Acc acc;
+  const uint64_t step = (uint64_t)gridDim.x * (K::BM * K::BN / 4);
+  const f32x4* from = reinterpret_cast<const f32x4*>(parts) +
+                      ((uint64_t)blockIdx.y * nparts * gridDim.x + blockIdx.x) * (K::BM * K::BN / 4) + threadIdx.x;
+#pragma unroll
+  for (int i = 0; i < K::MF; ++i)
+#pragma unroll
+    for (int j = 0; j < K::NF; ++j) acc[i][j] = from[(i * K::NF + j) * K::threads];
+  for (uint32_t z = 1; z < nparts; ++z)
+#pragma unroll
+    for (int i = 0; i < K::MF; ++i)
+#pragma unroll
+      for (int j = 0; j < K::NF; ++j) acc[i][j] += from[z * step + (i * K::NF + j) * K::threads];
+  sym_store<K, PAIR, KIND>(q, ws + blockIdx.y * q.bytes, ti, tj, ca, cb, cc, acc);
+}
+
 // X' = a X + B X into the other buffers, or, in the last step, into the
-// output.  First operand X as columns of k, second B (rows).
+// output (with pairs a is in B).  First operand X as columns of k, second B
+// (rows).
 template <DType T, class K, bool PAIR, bool LAST>
 __global__ __launch_bounds__(K::threads) void ortho_step(OrthoArgs a, OrthoMat q, char* ws, uint32_t cur, float ca,
                                                          uint32_t tm, uint32_t tn) {
   typedef typename Elem<T>::type E;
   __shared__ __attribute__((aligned(16))) char lds[K::lds_bytes];
   uint32_t m, n;
-  tile_of(blockIdx.x, tm, tn, 8, m, n);
-  char* base = ws + blockIdx.y * q.bytes;
+  const uint32_t item = xcd_share(blockIdx.x, gridDim.x), mat = uniform(item / (tm * tn));
+  tile_of(item - mat * (tm * tn), tm, tn, 8, m, n);
+  char* base = ws + mat * q.bytes;
   const uint32_t c0 = m * K::BM, r0 = n * K::BN;
   typename K::Acc acc = {};
   const Operand x{base + q.x[cur] + (uint64_t)c0 * (PAIR ? 4 : 2), q.xp, (int)(q.n - c0)};
   const Operand b{base + q.b + (uint64_t)r0 * q.ap, q.ap, (int)(q.m - r0)};
   K::run(x, b, q.m, lds_address(lds), acc);
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, wm = wave / K::WGN, wn = wave % K::WGN;
-  E* out = static_cast<E*>(a.out[blockIdx.y]);
+  E* out = static_cast<E*>(a.out[mat]);
   const bool tall = a.rows > a.cols;
   const uint32_t width = q.xp / (PAIR ? 4 : 2);
 #pragma unroll
   for (int j = 0; j < K::NF; ++j) {
     const uint32_t r = r0 + wn * K::WN + j * 16 + (lane & 15);
-    const uint64_t row = (uint64_t)r * q.xp;
+    const uint64_t row = (uint64_t)min(r, q.m - 1) * q.xp;
+    float old[K::MF][4];
+    if (!PAIR) {                         // all reads before the first store, which could alias them
+#pragma unroll
+      for (int i = 0; i < K::MF; ++i) {
+        const uint32_t c = min(c0 + wm * K::WM + i * 16 + 4 * (lane >> 4), width - 4);
+        get<PAIR>(base + q.x[cur] + row, base + q.lo[cur] + row, c, old[i]);
+      }
+    }
 #pragma unroll
     for (int i = 0; i < K::MF; ++i) {
       const uint32_t c = c0 + wm * K::WM + i * 16 + 4 * (lane >> 4);
       if (r >= q.m || c >= width) continue;
       float v[4];
-      get<PAIR>(base + q.x[cur] + row, base + q.lo[cur] + row, c, v);
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
-        v[e] = ca * v[e] + acc[i][j][e] * kInvScale;
+        v[e] = (PAIR ? 0.0f : ca * old[i][e]) + acc[i][j][e] * kInvScale;
         if (c + e >= q.n) v[e] = 0.0f;
       }
       if constexpr (LAST) {
@@ -259,6 +324,9 @@ template <bool PAIR, OperandKind A>
 using Big = TileMma<DType::F16, 256, 256, 2, 4, A, kRows, PAIR>;
 template <bool PAIR, OperandKind A>
 using Mid = TileMma<DType::F16, 128, 128, 2, 2, A, kRows, PAIR>;
+// one of these, alone on its CU, hides the loads behind three stages of them
+template <bool PAIR, OperandKind A>
+using Deep = TileMma<DType::F16, 128, 128, 2, 4, A, kRows, PAIR, 4>;
 template <bool PAIR, OperandKind A>
 using Small = TileMma<DType::F16, 64, 64, 2, 2, A, kRows, PAIR>;
 
@@ -289,61 +357,94 @@ OrthoMat layout(const OrthoArgs& a) {
 uint32_t ceil_div(uint32_t a, uint32_t b) { return (a + b - 1) / b; }
 
 template <class K, bool PAIR, SymKind KIND>
-void launch_sym(const OrthoMat& q, uint32_t nmat, char* ws, uint32_t cur, float cb, float cc, hipStream_t s) {
-  const uint32_t t = ceil_div(q.m, K::BM);
-  hipLaunchKernelGGL((ortho_sym<K, PAIR, KIND>), dim3(t * (t + 1) / 2, nmat), dim3(K::threads), 0, s, q, ws, cur, cb, cc);
+void launch_sym(const OrthoMat& q, uint32_t nmat, char* ws, float* parts, uint32_t cur, uint32_t splits, const float* c,
+                hipStream_t s) {
+  const uint32_t t = ceil_div(q.m, K::BM), k = KIND == kGram ? q.n : q.m;
+  const uint32_t share = (uint32_t)align_up(ceil_div(k, splits), 64);
+  const uint32_t tiles = t * (t + 1) / 2, shares = ceil_div(k, share);
+  hipLaunchKernelGGL((ortho_sym<K, PAIR, KIND>), dim3(tiles * shares * nmat), dim3(K::threads), 0, s, q, ws, parts, cur,
+                     tiles, shares, share, c[0], c[1], c[2]);
+  if (shares > 1)
+    hipLaunchKernelGGL((ortho_sym_join<K, PAIR, KIND>), dim3(tiles, nmat), dim3(K::threads), 0, s, q, ws, parts, shares,
+                       c[0], c[1], c[2]);
 }
 template <DType T, class K, bool PAIR>
 void launch_step(const OrthoArgs& a, const OrthoMat& q, char* ws, uint32_t cur, float ca, bool last, hipStream_t s) {
   const uint32_t tm = ceil_div(q.n, K::BM), tn = ceil_div(q.m, K::BN);
   if (last)
-    hipLaunchKernelGGL((ortho_step<T, K, PAIR, true>), dim3(tm * tn, a.nranks), dim3(K::threads), 0, s, a, q, ws, cur,
+    hipLaunchKernelGGL((ortho_step<T, K, PAIR, true>), dim3(tm * tn * a.nranks), dim3(K::threads), 0, s, a, q, ws, cur,
                        ca, tm, tn);
   else
-    hipLaunchKernelGGL((ortho_step<T, K, PAIR, false>), dim3(tm * tn, a.nranks), dim3(K::threads), 0, s, a, q, ws, cur,
+    hipLaunchKernelGGL((ortho_step<T, K, PAIR, false>), dim3(tm * tn * a.nranks), dim3(K::threads), 0, s, a, q, ws, cur,
                        ca, tm, tn);
 }
 
-// The largest tile that still gives every CU one.
-enum Shape { kBig, kMid, kSmall };
+constexpr uint32_t kSplitWork = 16384;
+
+// The tiles of a product, and into how many shares its k is split.
+enum Shape { kBig, kMid, kDeep, kSmall };
+struct Choice {
+  Shape shape;
+  uint32_t splits;
+};
+// The largest tile that still gives every CU one; 128 x 128 tiles are taken two
+// to a CU (kMid) or, if there are not that many, alone (kDeep).
 template <class F>
-Shape shape_of(int cus, uint32_t nmat, F tiles) {
-  if ((uint64_t)tiles(256u) * nmat >= (uint64_t)cus) return kBig;
-  return (uint64_t)tiles(128u) * nmat >= (uint64_t)cus ? kMid : kSmall;
+Choice choose(int cus, uint32_t nmat, F tiles) {
+  const uint64_t big = (uint64_t)tiles(256u) * nmat, mid = (uint64_t)tiles(128u) * nmat;
+  if (big >= (uint64_t)cus) return {kBig, 1};
+  if (mid > (uint64_t)cus) return {kMid, 1};
+  return {2 * mid >= (uint64_t)cus ? kDeep : kSmall, 1};
+}
+uint32_t triangle_tiles(uint32_t m, uint32_t b) {
+  const uint32_t t = ceil_div(m, b);
+  return t * (t + 1) / 2;
+}
+// A symmetric product over k.  Where 256 x 256 tiles are too few for the CUs,
+// their k is split so that about one round of workgroups fills them; that
+// takes a write and a read of the parts, so it needs a long k: at 2 x 2048 x
+// 8190 pairs 224 + 37 us against 335 us of 128 x 128 tiles, at 8 x 1024 x 4096
+// without pairs 53 + 26 us against 55 us.
+Choice choose_sym(const OrthoMat& q, int cus, uint32_t nmat, uint32_t k, bool pairs) {
+  const Choice c = choose(cus, nmat, [&](uint32_t b) { return triangle_tiles(q.m, b); });
+  const uint64_t big = (uint64_t)triangle_tiles(q.m, 256) * nmat;
+  if (c.shape == kBig || (uint64_t)k * (pairs ? 3 : 1) < kSplitWork) return c;
+  const uint32_t splits = (uint32_t)((uint64_t)cus / big);
+  if (splits < 2 || splits > 8 || big * splits * 5 < (uint64_t)cus * 4) return c;
+  return {kBig, splits};
 }
 
 template <DType T>
 hipError_t run(const OrthoArgs& a, char* workspace, hipStream_t s) {
   constexpr bool PAIR = T != DType::BF16;
   const OrthoMat q = layout(a);
-  double* parts = reinterpret_cast<double*>(workspace);
+  double* norms = reinterpret_cast<double*>(workspace);
   char* ws = workspace + align_up((size_t)a.nranks * q.parts * sizeof(double), 256);
-  hipLaunchKernelGGL(ortho_norm<T>, dim3(q.parts, a.nranks), dim3(256), 0, s, a, parts);
+  float* parts = reinterpret_cast<float*>(ws + a.nranks * q.bytes);
+  hipLaunchKernelGGL(ortho_norm<T>, dim3(q.parts, a.nranks), dim3(256), 0, s, a, norms);
   hipLaunchKernelGGL((ortho_load<T, PAIR>), dim3(ceil_div(q.xp / (PAIR ? 4 : 2), 64), ceil_div(q.m, 64), a.nranks), dim3(256),
-                     0, s, a, q, parts, ws);
-  const Shape sym = shape_of(a.cus, a.nranks, [&](uint32_t b) { const uint32_t t = ceil_div(q.m, b); return t * (t + 1) / 2; });
-  const Shape step = shape_of(a.cus, a.nranks, [&](uint32_t b) { return ceil_div(q.m, b) * ceil_div(q.n, b); });
+                     0, s, a, q, norms, ws);
+  const Choice gram = choose_sym(q, a.cus, a.nranks, q.n, PAIR), poly = choose_sym(q, a.cus, a.nranks, q.m, PAIR);
+  const Choice step = choose(a.cus, a.nranks, [&](uint32_t b) { return ceil_div(q.m, b) * ceil_div(q.n, b); });
+  auto sym = [&](auto kind, const Choice& w, uint32_t cur, const float* c) {
+    constexpr SymKind KIND = decltype(kind)::value;
+    switch (w.shape) {
+      case kBig: launch_sym<Big<PAIR, kRows>, PAIR, KIND>(q, a.nranks, ws, parts, cur, w.splits, c, s); break;
+      case kMid: launch_sym<Mid<PAIR, kRows>, PAIR, KIND>(q, a.nranks, ws, parts, cur, w.splits, c, s); break;
+      case kDeep: launch_sym<Deep<PAIR, kRows>, PAIR, KIND>(q, a.nranks, ws, parts, cur, w.splits, c, s); break;
+      default: launch_sym<Small<PAIR, kRows>, PAIR, KIND>(q, a.nranks, ws, parts, cur, w.splits, c, s); break;
+    }
+  };
   uint32_t cur = 0;
   for (int i = 0; i < a.steps; ++i, cur ^= 1) {
     const float* c = a.coeffs + 3 * i;
     const bool last = i + 1 == a.steps;
-    switch (sym) {
-      case kBig:
-        launch_sym<Big<PAIR, kRows>, PAIR, kGram>(q, a.nranks, ws, cur, 0.0f, 0.0f, s);
-        launch_sym<Big<PAIR, kRows>, PAIR, kPoly>(q, a.nranks, ws, cur, c[1], c[2], s);
-        break;
-      case kMid:
-        launch_sym<Mid<PAIR, kRows>, PAIR, kGram>(q, a.nranks, ws, cur, 0.0f, 0.0f, s);
-        launch_sym<Mid<PAIR, kRows>, PAIR, kPoly>(q, a.nranks, ws, cur, c[1], c[2], s);
-        break;
-      default:
-        launch_sym<Small<PAIR, kRows>, PAIR, kGram>(q, a.nranks, ws, cur, 0.0f, 0.0f, s);
-        launch_sym<Small<PAIR, kRows>, PAIR, kPoly>(q, a.nranks, ws, cur, c[1], c[2], s);
-        break;
-    }
-    switch (step) {
+    sym(std::integral_constant<SymKind, kGram>(), gram, cur, c);
+    sym(std::integral_constant<SymKind, kPoly>(), poly, cur, c);
+    switch (step.shape) {
       case kBig: launch_step<T, Big<PAIR, kCols>, PAIR>(a, q, ws, cur, c[0], last, s); break;
       case kMid: launch_step<T, Mid<PAIR, kCols>, PAIR>(a, q, ws, cur, c[0], last, s); break;
+      case kDeep: launch_step<T, Deep<PAIR, kCols>, PAIR>(a, q, ws, cur, c[0], last, s); break;
       default: launch_step<T, Small<PAIR, kCols>, PAIR>(a, q, ws, cur, c[0], last, s); break;
     }
   }
@@ -354,7 +455,12 @@ hipError_t run(const OrthoArgs& a, char* workspace, hipStream_t s) {
 
 size_t ortho_space(const OrthoArgs& a) {
   const OrthoMat q = layout(a);
-  return align_up((size_t)a.nranks * q.parts * sizeof(double), 256) + (size_t)a.nranks * q.bytes;
+  size_t parts = 0;
+  for (uint32_t k : {q.n, q.m}) {
+    const Choice c = choose_sym(q, a.cus, a.nranks, k, pairs(a.type));
+    if (c.splits > 1) parts = std::max(parts, (size_t)c.splits * a.nranks * triangle_tiles(q.m, 256) * (256 * 256 * sizeof(float)));
+  }
+  return align_up((size_t)a.nranks * q.parts * sizeof(double), 256) + (size_t)a.nranks * q.bytes + parts;
 }
 
 int orthogonalize(const OrthoArgs& a, char* workspace, void* stream) {

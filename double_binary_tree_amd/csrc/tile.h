@@ -6,8 +6,8 @@
 // Staging.  One k-step covers 128 bytes of k per row (64 16-bit or 32 f32
 // values), so a stage holds 128 bytes times BM + BN whatever the layout.  It
 // goes from global memory straight to LDS, 16 bytes a lane, 1 KiB a wave
-// access; two stages alternate, so the loads of step s + 1 run while step s is
-// multiplied.  LDS is filled in lane order, so the permutations below are
+// access; STAGES stages rotate, so the loads of the STAGES - 1 steps after s run
+// while step s is multiplied.  LDS is filled in lane order, so the permutations below are
 // applied to the global addresses.
 //   kRows: a wave access holds 8 rows of 128 bytes.  The 16-byte chunk c of
 //     row r sits at chunk c ^ ((r >> 1) & 7): the 16 rows that a matrix
@@ -85,8 +85,12 @@ __device__ __forceinline__ void load_to_lds(const char* base, uint32_t off, uint
   asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2" ::"s"(lds), "v"(off), "s"(base)
                : "memory");
 }
-// This wave's loads to LDS have all arrived (other waves': after a barrier).
-__device__ __forceinline__ void lds_arrived() { asm volatile("s_waitcnt vmcnt(0)" ::: "memory"); }
+// At most N of this wave's loads to LDS have not arrived yet (other waves':
+// after a barrier).
+template <int N>
+__device__ __forceinline__ void lds_arrived() {
+  asm volatile("s_waitcnt vmcnt(%0)" ::"n"(N) : "memory");
+}
 // LDS by byte address (an address-space cast of a generic pointer per access
 // would leave the compiler with flat accesses).
 typedef __attribute__((address_space(3))) u32x4 LdsVec;
@@ -186,7 +190,8 @@ struct Side {
 // BM x BN by WGM x WGN waves, each wave MF x NF fragments of 16 x 16.
 // acc[i][j] of a lane holds C[m][n] at m = 16 i + 4 (lane >> 4) + e, n = 16 j
 // + (lane & 15) of the wave's part, e = 0 .. 3.
-template <DType T, int BM_, int BN_, int WGM_, int WGN_, OperandKind KA = kRows, OperandKind KB = kRows, bool PAIR = false>
+template <DType T, int BM_, int BN_, int WGM_, int WGN_, OperandKind KA = kRows, OperandKind KB = kRows, bool PAIR = false,
+          int STAGES = 2>
 struct TileMma {
   static constexpr int BM = BM_, BN = BN_, WGM = WGM_, WGN = WGN_;
   static constexpr int waves = WGM * WGN, threads = 64 * waves;
@@ -195,7 +200,8 @@ struct TileMma {
   typedef Side<T, BN, KB, PAIR, waves> SB;
   static constexpr int kstep = SA::kstep;
   static constexpr int stage_bytes = SA::bytes + SB::bytes;
-  static constexpr int lds_bytes = 2 * stage_bytes;
+  static constexpr int lds_bytes = STAGES * stage_bytes;
+  static constexpr int loads = SA::loads + SB::loads;       // per wave and step
   using Acc = f32x4[MF][NF];
 
   static __device__ __forceinline__ void multiply(uint32_t lds, int wm, int wn, int lane, const typename SA::Frag& pa,
@@ -250,8 +256,8 @@ struct TileMma {
     for (int l = 0; l < SB::loads; ++l) SB::place(b, wave, lane, l, kstep, ob[l]);
     const uint64_t da = SA::advance(a), db = SB::advance(b);
     auto fetch = [&](uint32_t s) {
-      const uint32_t to = lds + (s & 1) * stage_bytes + wave * (SA::loads * 1024);
-      const uint32_t tob = lds + (s & 1) * stage_bytes + SA::bytes + wave * (SB::loads * 1024);
+      const uint32_t at = lds + s % STAGES * stage_bytes;
+      const uint32_t to = at + wave * (SA::loads * 1024), tob = at + SA::bytes + wave * (SB::loads * 1024);
       const bool whole = s + 1 < steps || left == kstep;
 #pragma unroll
       for (int l = 0; l < SA::loads; ++l) {
@@ -268,14 +274,16 @@ struct TileMma {
       a.base += da;
       b.base += db;
     };
-    fetch(0);
+#pragma unroll
+    for (uint32_t s = 0; s < STAGES - 1; ++s)
+      if (s < steps) fetch(s);
     for (uint32_t s = 0; s < steps; ++s) {
-      lds_arrived();
-      __syncthreads();     // step s is in LDS; every wave is done with the other stage
-      const uint32_t at = lds + (s & 1) * stage_bytes;
-      if (s + 1 < steps) {
-        fetch(s + 1);
-      } else if (left != kstep) {
+      if (s + STAGES <= steps + 1) lds_arrived<(STAGES - 2) * loads>();
+      else lds_arrived<0>();
+      __syncthreads();     // step s is in LDS; every wave is done with the stage of s - 1
+      const uint32_t at = lds + s % STAGES * stage_bytes;
+      if (s + STAGES - 1 < steps) fetch(s + STAGES - 1);
+      if (s + 1 == steps && left != kstep) {
         const u32x4 zero = {0, 0, 0, 0};
         uint32_t unused;
 #pragma unroll
@@ -292,17 +300,25 @@ struct TileMma {
   }
 };
 
-// Workgroup -> tile.  Consecutive workgroups go to the 8 XCDs in turn, so
-// workgroup w of `total` is taken as the (w / 8)-th of XCD w % 8's contiguous
-// share, and the tiles are walked in bands of `band` tile rows: the tiles
-// that one XCD works on at a time share rows of both operands in its L2.
-__device__ __forceinline__ void tile_of(uint32_t w, uint32_t tm, uint32_t tn, uint32_t band, uint32_t& m, uint32_t& n) {
-  const uint32_t total = tm * tn, x = w & 7, q = total >> 3, rem = total & 7;
-  uint32_t t = x * q + min(x, rem) + (w >> 3);
+// A value that is the same in every lane, in a scalar register (the compiler
+// divides in vector registers, and addresses of LDS loads have to be scalar).
+__device__ __forceinline__ uint32_t uniform(uint32_t x) { return (uint32_t)__builtin_amdgcn_readfirstlane((int)x); }
+
+// Workgroup -> work item.  Consecutive workgroups go to the 8 XCDs in turn, so
+// workgroup w of `total` takes the (w / 8)-th item of XCD w % 8's contiguous
+// share: neighbouring items run on one XCD and meet in its L2.
+__device__ __forceinline__ uint32_t xcd_share(uint32_t w, uint32_t total) {
+  const uint32_t x = w & 7, q = total >> 3, rem = total & 7;
+  return x * q + min(x, rem) + (w >> 3);
+}
+
+// Item t of tm x tn tiles, walked in bands of `band` tile rows: the tiles that
+// one XCD works on at a time share rows of both operands.
+__device__ __forceinline__ void tile_of(uint32_t t, uint32_t tm, uint32_t tn, uint32_t band, uint32_t& m, uint32_t& n) {
   const uint32_t per = band * tn, g = t / per, first = g * band, rows = min(band, tm - first);
   t -= g * per;
-  m = first + t % rows;
-  n = t / rows;
+  n = uniform(t / rows);
+  m = uniform(first + t % rows);
 }
 
 }  // namespace emu

@@ -72,7 +72,7 @@ __global__ __launch_bounds__(K::threads) void xent_stats(Shards sh, LossTile p) 
   __shared__ __attribute__((aligned(16))) char lds[K::lds_bytes];
   constexpr int ES = sizeof(typename Elem<T>::type);
   uint32_t m, n;
-  tile_of(blockIdx.x, p.tm, p.tn, p.band, m, n);
+  tile_of(xcd_share(blockIdx.x, gridDim.x), p.tm, p.tn, p.band, m, n);
   const uint32_t tile = m, r = rank_of_tile(sh, K::BM, m);
   const uint32_t ld = p.dim * ES, row = m * K::BM, tok = n * K::BN;
   const int rows = (int)(sh.rows[r] - row);
@@ -125,26 +125,31 @@ __global__ __launch_bounds__(K::threads) void xent_stats(Shards sh, LossTile p) 
   }
 }
 
-// 16 tokens a workgroup, 16 lanes each: lane k merges a contiguous share of
-// the tiles, and the 16 shares are merged in order.
-constexpr int kJoin = 16;
-__global__ __launch_bounds__(kJoin* kJoin) void xent_join(const float2* __restrict__ stats, const float* __restrict__ label,
-                                                         const int64_t* __restrict__ targets, uint32_t tokens,
-                                                         uint32_t tiles, int64_t vocab, float* __restrict__ loss,
-                                                         float* __restrict__ lse) {
-  __shared__ float2 part[kJoin][kJoin];
-  const uint32_t c = threadIdx.x % kJoin, k = threadIdx.x / kJoin, t = blockIdx.x * kJoin + c;
-  const uint32_t share = (tiles + kJoin - 1) / kJoin;
+// 16 tokens a workgroup, 64 lanes each: lane k merges a contiguous share of
+// the tiles, and the 64 shares are merged in order.  (16 lanes each took 30 us
+// for 48 tokens x 1001 tiles, as long as a fifth of the product itself.)
+constexpr int kJoinTokens = 16, kJoinLanes = 64;
+__global__ __launch_bounds__(kJoinTokens* kJoinLanes) void xent_join(
+    const float2* __restrict__ stats, const float* __restrict__ label, const int64_t* __restrict__ targets, uint32_t tokens,
+    uint32_t tiles, int64_t vocab, float* __restrict__ loss, float* __restrict__ lse) {
+  __shared__ float2 part[kJoinLanes][kJoinTokens];
+  const uint32_t c = threadIdx.x % kJoinTokens, k = threadIdx.x / kJoinTokens, t = blockIdx.x * kJoinTokens + c;
+  const uint32_t share = (tiles + kJoinLanes - 1) / kJoinLanes, end = min((k + 1) * share, tiles);
   float m = -INFINITY, s = 0.0f;
+  constexpr uint32_t kBatch = 8;         // loads under way at a time
   if (t < tokens)
-    for (uint32_t i = k * share; i < min((k + 1) * share, tiles); ++i) {
-      const float2 q = stats[(uint64_t)i * tokens + t];
-      merge(m, s, q.x, q.y);
+    for (uint32_t i = k * share; i < end; i += kBatch) {
+      float2 q[kBatch];
+#pragma unroll
+      for (uint32_t j = 0; j < kBatch; ++j) q[j] = stats[(uint64_t)min(i + j, end - 1) * tokens + t];
+#pragma unroll
+      for (uint32_t j = 0; j < kBatch; ++j)
+        if (i + j < end) merge(m, s, q[j].x, q[j].y);
     }
   part[k][c] = make_float2(m, s);
   __syncthreads();
   if (k == 0 && t < tokens) {
-    for (int i = 1; i < kJoin; ++i) merge(m, s, part[i][c].x, part[i][c].y);
+    for (int i = 1; i < kJoinLanes; ++i) merge(m, s, part[i][c].x, part[i][c].y);
     const float l = m + logf(s);
     const int64_t y = targets[t];
     lse[t] = l;
@@ -211,7 +216,7 @@ __global__ __launch_bounds__(K::threads) void xent_dlogits(Shards sh, GradTile p
   typedef E E4 __attribute__((ext_vector_type(4)));
   constexpr int ES = sizeof(E);
   uint32_t m, n;
-  tile_of(blockIdx.x, p.tm, p.tn, p.band, m, n);
+  tile_of(xcd_share(blockIdx.x, gridDim.x), p.tm, p.tn, p.band, m, n);
   const uint32_t r = rank_of_tile(sh, K::BM, m);
   const uint32_t ld = p.dim * ES, row = m * K::BM, tok = n * K::BN;
   const int rows = (int)(sh.rows[r] - row);
@@ -261,7 +266,7 @@ __global__ __launch_bounds__(K::threads) void xent_dx(Shards sh, DxTile p) {
   __shared__ __attribute__((aligned(16))) char lds[K::lds_bytes];
   constexpr int ES = sizeof(typename Elem<T>::type);
   uint32_t m, n;
-  tile_of(blockIdx.x, p.tm, p.tn, p.band, m, n);
+  tile_of(xcd_share(blockIdx.x, gridDim.x), p.tm, p.tn, p.band, m, n);
   const uint32_t k0 = blockIdx.y * p.share, k1 = k0 + p.share;
   const uint32_t col = m * K::BM, tok = n * K::BN, wld = p.dim * ES, gld = p.vpitch * ES;
   typename K::Acc acc = {};
@@ -282,13 +287,18 @@ __global__ __launch_bounds__(K::threads) void xent_dx(Shards sh, DxTile p) {
 #pragma unroll
   for (int j = 0; j < K::NF; ++j) {
     const uint32_t t = tok + wn * K::WN + j * 16 + (lane & 15);
+    const uint32_t d0 = col + wm * K::WM + 4 * (lane >> 4);
+    float* row = part + (uint64_t)min(t, p.tokens - 1) * p.dim;
+    if (p.add) {                         // all reads before the first store, which could alias them
+      f32x4 old[K::MF];
 #pragma unroll
-    for (int i = 0; i < K::MF; ++i) {
-      const uint32_t d = col + wm * K::WM + i * 16 + 4 * (lane >> 4);
-      if (t >= p.tokens || d >= p.dim) continue;
-      f32x4* at = reinterpret_cast<f32x4*>(part + (uint64_t)t * p.dim + d);
-      *at = p.add ? *at + acc[i][j] : acc[i][j];
+      for (int i = 0; i < K::MF; ++i) old[i] = *reinterpret_cast<const f32x4*>(row + min(d0 + i * 16, p.dim - 4));
+#pragma unroll
+      for (int i = 0; i < K::MF; ++i) acc[i][j] += old[i];
     }
+#pragma unroll
+    for (int i = 0; i < K::MF; ++i)
+      if (t < p.tokens && d0 + i * 16 < p.dim) *reinterpret_cast<f32x4*>(row + d0 + i * 16) = acc[i][j];
   }
 }
 
@@ -336,7 +346,7 @@ __global__ __launch_bounds__(K::threads) void xent_dw(Shards sh, DwTile p) {
   typedef E E4 __attribute__((ext_vector_type(4)));
   constexpr int ES = sizeof(E);
   uint32_t m, n;
-  tile_of(blockIdx.x, p.tm, p.tn, p.band, m, n);
+  tile_of(xcd_share(blockIdx.x, gridDim.x), p.tm, p.tn, p.band, m, n);
   const uint32_t r = rank_of_tile(sh, K::BN, n), col = m * K::BM, row = n * K::BN;
   const Operand a{static_cast<const char*>(p.x) + (uint64_t)col * ES, p.dim * ES, (int)(p.dim - col)};
   const Operand b{static_cast<const char*>(p.g) + (uint64_t)(sh.first[r] + row) * ES, p.vpitch * ES, (int)(sh.rows[r] - row)};
@@ -367,21 +377,38 @@ using Big = TileMma<T, 256, 256, 2, 4, A, B>;
 template <DType T, OperandKind A = kRows, OperandKind B = kRows>
 using Mid = TileMma<T, 128, 128, 2, 2, A, B>;
 template <DType T, OperandKind A = kRows, OperandKind B = kRows>
-using Thin = TileMma<T, 128, 64, 4, 1, A, B>;
+using Small = TileMma<T, 64, 64, 2, 2, A, B>;
+template <DType T, OperandKind A = kRows, OperandKind B = kRows>
+using Thin = TileMma<T, 128, 64, 4, 1, A, B, false, 3>;    // reads rows at 5.6 TB/s; two stages 5.1, four 5.4
 
 uint32_t ceil_div(uint32_t a, uint32_t b) { return (a + b - 1) / b; }
 
-// Large tiles once they fill every CU, else the small ones; never more than
-// twice the width of the second operand (the tokens).
-enum Shape { kBig, kMid, kThin };
-Shape shape_of(uint64_t big_tiles, uint32_t second, int cus) {
-  if (second <= 64) return kThin;
-  return second > 128 && big_tiles >= (uint64_t)cus ? kBig : kMid;
+// The largest tile that still gives every CU a workgroup (128 x 128: two, as
+// they run two to a CU), for up to 64 tokens the one that is 64 wide.  At 301
+// tokens, 8009 rows, 520 wide in f32 the three products of a gradient take
+// 36 + 34 + 40 us with 64 x 64 tiles, 48 + 50 + 52 us with 128 x 128.
+enum Shape { kBig, kMid, kThin, kSmall };
+template <class F>
+Shape shape_of(uint32_t tokens, int cus, F tiles) {
+  if (tokens > 128 && tiles(256u) >= (uint64_t)cus) return kBig;
+  if (tokens <= 64) return kThin;
+  return tiles(128u) >= 2 * (uint64_t)cus ? kMid : kSmall;
 }
-constexpr uint32_t kBmOf[] = {256, 128, 128};
+constexpr uint32_t kBmOf[] = {256, 128, 128, 64};
 
-Shape loss_shape(const XentArgs& a, const Shards& s) {
-  return shape_of((uint64_t)tiles_of(s, 256) * ceil_div(a.tokens, 256), a.tokens, a.cus);
+// Calls f with the tile type of a shape.
+template <DType T, OperandKind A, OperandKind B, class F>
+hipError_t with_tile(Shape s, F f) {
+  switch (s) {
+    case kBig: return f(Big<T, A, B>());
+    case kMid: return f(Mid<T, A, B>());
+    case kThin: return f(Thin<T, A, B>());
+    default: return f(Small<T, A, B>());
+  }
+}
+
+Shape logits_shape(const XentArgs& a, const Shards& s) {
+  return shape_of(a.tokens, a.cus, [&](uint32_t b) { return (uint64_t)tiles_of(s, b) * ceil_div(a.tokens, b); });
 }
 
 template <DType T, class K>
@@ -397,16 +424,13 @@ hipError_t loss_of(const XentArgs& a, const Shards& sh, char* ws, hipStream_t s)
   float2* stats = reinterpret_cast<float2*>(ws + m.stats);
   float* label = reinterpret_cast<float*>(ws + m.label);
   uint32_t tiles = 0;
-  hipError_t e;
-  switch (loss_shape(a, sh)) {
-    case kBig: e = launch_stats<T, Big<T>>(a, sh, stats, label, &tiles, s); break;
-    case kMid: e = launch_stats<T, Mid<T>>(a, sh, stats, label, &tiles, s); break;
-    default: e = launch_stats<T, Thin<T>>(a, sh, stats, label, &tiles, s); break;
-  }
+  const hipError_t e = with_tile<T, kRows, kRows>(logits_shape(a, sh), [&](auto k) {
+    return launch_stats<T, decltype(k)>(a, sh, stats, label, &tiles, s);
+  });
   if (e) return e;
   int64_t vocab = 0;
   for (uint32_t r = 0; r < sh.nranks; ++r) vocab += sh.rows[r];
-  hipLaunchKernelGGL(xent_join, dim3(ceil_div(a.tokens, kJoin)), dim3(kJoin * kJoin), 0, s, stats, label, a.targets,
+  hipLaunchKernelGGL(xent_join, dim3(ceil_div(a.tokens, kJoinTokens)), dim3(kJoinTokens * kJoinLanes), 0, s, stats, label, a.targets,
                      a.tokens, tiles, vocab, a.loss, a.lse);
   return hipGetLastError();
 }
@@ -466,7 +490,8 @@ hipError_t launch_dw(const Shards& run, DwTile p, hipStream_t s) {
 }
 
 Shape dx_shape(const XentArgs& a, uint32_t splits) {
-  return shape_of((uint64_t)ceil_div(a.dim, 256) * ceil_div(a.tokens, 256) * splits, a.tokens, a.cus);
+  return shape_of(a.tokens, a.cus,
+                  [&](uint32_t b) { return (uint64_t)ceil_div(a.dim, b) * ceil_div(a.tokens, b) * splits; });
 }
 
 template <DType T>
@@ -506,11 +531,8 @@ hipError_t grad_of(const XentArgs& a, const Shards& all, char* ws, hipStream_t s
   bool add = false;
   while (at < (uint64_t)vocab) {
     const Shards run = next_run(all, m.width, at);
-    switch (shape_of((uint64_t)tiles_of(run, 256) * ceil_div(a.tokens, 256), a.tokens, a.cus)) {
-      case kBig: e = launch_dlogits<T, Big<T>>(a, run, gp, s); break;
-      case kMid: e = launch_dlogits<T, Mid<T>>(a, run, gp, s); break;
-      default: e = launch_dlogits<T, Thin<T>>(a, run, gp, s); break;
-    }
+    e = with_tile<T, kRows, kRows>(logits_shape(a, run),
+                                   [&](auto k) { return launch_dlogits<T, decltype(k)>(a, run, gp, s); });
     if (e) return e;
     if (dx) {
       DxTile p{};
@@ -522,11 +544,8 @@ hipError_t grad_of(const XentArgs& a, const Shards& all, char* ws, hipStream_t s
       p.share = (uint32_t)align_up(ceil_div(run.width, m.splits), 64);
       p.add = add;
       add = true;
-      switch (dx_shape(a, m.splits)) {
-        case kBig: e = launch_dx<T, Big<T, kCols, kRows>>(run, p, m.splits, s); break;
-        case kMid: e = launch_dx<T, Mid<T, kCols, kRows>>(run, p, m.splits, s); break;
-        default: e = launch_dx<T, Thin<T, kCols, kRows>>(run, p, m.splits, s); break;
-      }
+      e = with_tile<T, kCols, kRows>(dx_shape(a, m.splits),
+                                     [&](auto k) { return launch_dx<T, decltype(k)>(run, p, m.splits, s); });
       if (e) return e;
     }
     if (dw) {
@@ -537,8 +556,10 @@ hipError_t grad_of(const XentArgs& a, const Shards& all, char* ws, hipStream_t s
       p.tokens = a.tokens;
       p.dim = a.dim;
       p.vpitch = m.vpitch;
-      if ((uint64_t)ceil_div(a.dim, 256) * tiles_of(run, 256) >= (uint64_t)a.cus) e = launch_dw<T, Big<T, kCols, kCols>>(run, p, s);
-      else e = launch_dw<T, Mid<T, kCols, kCols>>(run, p, s);
+      // its second operand is the vocabulary: never the narrow tile
+      const Shape shape = shape_of(a.tokens <= 64 ? 128 : a.tokens, a.cus,
+                                   [&](uint32_t b) { return (uint64_t)ceil_div(a.dim, b) * tiles_of(run, b); });
+      e = with_tile<T, kCols, kCols>(shape, [&](auto k) { return launch_dw<T, decltype(k)>(run, p, s); });
       if (e) return e;
     }
   }
@@ -555,21 +576,21 @@ hipError_t grad_of(const XentArgs& a, const Shards& all, char* ws, hipStream_t s
 
 XentLossSpace xent_loss_space(const XentArgs& a, const Shards& all) {
   XentLossSpace m;
-  const uint32_t tiles = tiles_of(all, kBmOf[loss_shape(a, all)]);
+  const uint32_t tiles = tiles_of(all, kBmOf[logits_shape(a, all)]);
   m.stats = 0;
   m.label = align_up((size_t)tiles * a.tokens * sizeof(float2), 256);
   m.bytes = m.label + align_up((size_t)a.tokens * sizeof(float), 256);
   return m;
 }
 
-// A run takes as many positions as keep g within 2^27 values, at least 4096; dx is split over the width of a run until its
+// A run takes as many positions as keep g within 2^28 values, at least 4096 (2^27: 3% slower at 8192 x 100277 x 4096); dx is split over the width of a run until its
 // tiles reach two per CU, at most 64 ways.
 XentGradSpace xent_grad_space(const XentArgs& a, const Shards& all, bool dx, bool dw) {
   XentGradSpace m;
   const size_t es = (size_t)elem_size(a.type);
   uint64_t positions = 0;
   for (uint32_t r = 0; r < all.nranks; ++r) positions += align_up(all.rows[r], kShardAlign);
-  m.width = (uint32_t)std::min<uint64_t>(positions, std::max<uint64_t>(4096, (((uint64_t)1 << 27) / a.tokens) / 256 * 256));
+  m.width = (uint32_t)std::min<uint64_t>(positions, std::max<uint64_t>(4096, (((uint64_t)1 << 28) / a.tokens) / 256 * 256));
   m.vpitch = (uint32_t)align_up(m.width, 64);
   const uint64_t tiles = (uint64_t)ceil_div(a.dim, 128) * ceil_div(a.tokens, 128);
   while (m.splits < 64 && tiles * m.splits < 2 * (uint64_t)a.cus && m.width / (2 * m.splits) >= 256) m.splits *= 2;
