@@ -266,6 +266,38 @@ __global__ __launch_bounds__(K::threads) void ortho_sym_join(OrthoMat q, char* w
   sym_store<K, PAIR, KIND>(q, ws + blockIdx.y * q.bytes, ti, tj, ca, cb, cc, acc);
 }
 
+// A tile's results, v[i][j] as in TileMma, as pairs into rows of a state matrix:
+// rows j along the columns i (origin: the tile's first row and column).  `width`
+// columns are left from the tile's first one (whole vectors), `rows` rows.
+template <class K>
+__device__ __forceinline__ void store_pairs(uint32_t lds, const typename K::Acc& v, char* origin, uint32_t pitch, int rows, int width) {
+  const int lane = threadIdx.x & 63, wave = uniform(threadIdx.x >> 6), wm = wave / K::WGN, wn = wave % K::WGN;
+  constexpr int JP = K::NF / 2;          // the wave's share of LDS holds half of its pairs
+  const RowStage<K, K::WM * 4, JP * 16> stage(lds, wave, lane);
+  __syncthreads();
+#pragma unroll
+  for (int q = 0; q < 2; ++q) {
+#pragma unroll
+    for (int j = 0; j < JP; ++j)
+#pragma unroll
+      for (int i = 0; i < K::MF; ++i) {
+        f16x4 hi, lo;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          _Float16 h, l;
+          split(v[i][q * JP + j][e], h, l);
+          hi[e] = h;
+          lo[e] = l;
+        }
+        const uint32_t at = column<true>(i * 16 + 4 * (lane >> 4));
+        stage.put(j * 16 + (lane & 15), at, hi);
+        stage.put(j * 16 + (lane & 15), at + 64, lo);
+      }
+    const int row = wn * K::WN + q * JP * 16;
+    stage.store(origin + (uint64_t)row * pitch + wm * K::WM * 4, pitch, rows - row, (width - wm * K::WM) * 4);
+  }
+}
+
 // X' = a X + B X into the other buffers, or, in the last step, into the
 // output (with pairs a is in B).  First operand X as columns of k, second B
 // (rows).
@@ -287,6 +319,17 @@ __global__ __launch_bounds__(K::threads) void ortho_step(OrthoArgs a, OrthoMat q
   E* out = static_cast<E*>(a.out[mat]);
   const bool tall = a.rows > a.cols;
   const uint32_t width = q.xp / (PAIR ? 4 : 2);
+  if constexpr (PAIR && !LAST) {
+#pragma unroll
+    for (int i = 0; i < K::MF; ++i)
+#pragma unroll
+      for (int j = 0; j < K::NF; ++j)
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          acc[i][j][e] = c0 + wm * K::WM + i * 16 + 4 * (lane >> 4) + e < q.n ? acc[i][j][e] * kInvScale : 0.0f;
+    store_pairs<K>(lds_address(lds), acc, base + q.x[cur ^ 1] + (uint64_t)r0 * q.xp + c0 * 4, q.xp, (int)(q.m - r0), (int)(width - c0));
+    return;
+  }
 #pragma unroll
   for (int j = 0; j < K::NF; ++j) {
     const uint32_t r = r0 + wn * K::WN + j * 16 + (lane & 15);

@@ -300,6 +300,58 @@ struct TileMma {
   }
 };
 
+// Results by rows.  A lane's four results are consecutive in m, the rows of a
+// 16-bit matrix run along m, and 16 lanes hold 16 rows: stored as they are, one
+// access would touch 16 rows 32 bytes each.  A wave instead collects R rows of
+// RB bytes of its part in its share of LDS (WM * WN * 2 bytes; every wave must
+// be done with the product's stages) and moves them 16 bytes a lane, RB
+// contiguous bytes a row.  The 16-byte chunks of a row are permuted by its
+// number, so that the 16 rows of a store into LDS do not meet in one bank.
+template <class K, int RB, int R>
+struct RowStage {
+  static_assert(RB * R <= K::WM * K::WN * 2, "a wave's share of LDS");
+  static constexpr int CH = RB / 16, moves = RB * R / 1024;
+  static_assert(moves * 1024 == RB * R, "whole wave accesses");
+  uint32_t region;
+  int lane;
+  __device__ __forceinline__ RowStage(uint32_t lds, int wave, int lane_) : region(lds + wave * (K::WM * K::WN * 2)), lane(lane_) {}
+  static __device__ __forceinline__ uint32_t mix(uint32_t row) {
+    return RB >= 256 ? row & 15 : RB == 128 ? (row >> 1) & 7 : (row >> 2) & 3;
+  }
+  __device__ __forceinline__ uint32_t at(uint32_t row, uint32_t byte) const {
+    return region + row * RB + ((byte >> 4 ^ mix(row)) << 4) + (byte & 15);
+  }
+  typedef unsigned int u32x2 __attribute__((ext_vector_type(2)));
+  template <class V>
+  __device__ __forceinline__ void put(uint32_t row, uint32_t byte, V v) const {
+    *(__attribute__((address_space(3))) V*)(uintptr_t)at(row, byte) = v;
+  }
+  template <class V>
+  __device__ __forceinline__ V get(uint32_t row, uint32_t byte) const {
+    return *(const __attribute__((address_space(3))) V*)(uintptr_t)at(row, byte);
+  }
+  // Stores the rows at base + row * pitch: `rows` rows of `bytes` bytes (a
+  // multiple of 16; neither need be positive).
+  __device__ __forceinline__ void store(char* base, uint64_t pitch, int rows, int bytes) const {
+#pragma unroll
+    for (int i = 0; i < moves; ++i) {
+      const int at = i * 64 + lane, row = at / CH, c = at % CH;
+      const u32x4 v = lds_read(region + row * RB + ((c ^ mix(row)) << 4));
+      if (row < rows && c * 16 < bytes) *reinterpret_cast<u32x4*>(base + row * pitch + c * 16) = v;
+    }
+  }
+  // Loads them (places outside read some place inside; rows, bytes > 0); `base`
+  // uniform, and rows * pitch below 2^32.
+  __device__ __forceinline__ void load(const char* base, uint32_t pitch, int rows, int bytes) const {
+    asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");      // earlier reads of the region are back
+#pragma unroll
+    for (int i = 0; i < moves; ++i) {
+      const int at = i * 64 + lane, row = at / CH, c = at % CH ^ (int)mix(row);
+      load_to_lds(base, (uint32_t)min(row, rows - 1) * pitch + (uint32_t)min(c * 16, bytes - 16), region + i * 1024);
+    }
+  }
+};
+
 // A value that is the same in every lane, in a scalar register (the compiler
 // divides in vector registers, and addresses of LDS loads have to be scalar).
 __device__ __forceinline__ uint32_t uniform(uint32_t x) { return (uint32_t)__builtin_amdgcn_readfirstlane((int)x); }

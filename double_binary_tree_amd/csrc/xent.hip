@@ -230,6 +230,8 @@ __global__ __launch_bounds__(K::threads) void xent_dlogits(Shards sh, GradTile p
   const float scale = p.scale ? p.scale[0] : 1.0f;
   const uint32_t first = sh.first[r] + row;
   E* g = static_cast<E*>(p.g);
+  const RowStage<K, K::WM * 2, K::WN> stage(lds_address(lds), wave, lane);
+  if constexpr (ES == 2) __syncthreads();
 #pragma unroll
   for (int j = 0; j < K::NF; ++j) {
     const uint32_t t = tok + wn * K::WN + j * 16 + (lane & 15), tt = min(t, p.tokens - 1);
@@ -247,9 +249,13 @@ __global__ __launch_bounds__(K::threads) void xent_dlogits(Shards sh, GradTile p
         const float q = exp_of(acc[i][j][e] - lse) - (v + e == y ? 1.0f : 0.0f);
         out[e] = (E)(counted && v + e < rows ? d * q : 0.0f);
       }
-      if (v < padded && t < p.tokens) *reinterpret_cast<E4*>(g + (uint64_t)t * p.vpitch + first + v) = out;
+      if constexpr (ES == 2) stage.put(j * 16 + (lane & 15), (i * 16 + 4 * (lane >> 4)) * 2, out);
+      else if (v < padded && t < p.tokens) *reinterpret_cast<E4*>(g + (uint64_t)t * p.vpitch + first + v) = out;
     }
   }
+  if constexpr (ES == 2)
+    stage.store(reinterpret_cast<char*>(g + (uint64_t)(tok + wn * K::WN) * p.vpitch + first + wm * K::WM), (uint64_t)p.vpitch * ES,
+                (int)(p.tokens - tok) - wn * K::WN, (padded - wm * K::WM) * ES);
 }
 
 // dx: first operand the run's rows as they lie in memory (columns of k), second
@@ -355,19 +361,24 @@ __global__ __launch_bounds__(K::threads) void xent_dw(Shards sh, DwTile p) {
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, wm = wave / K::WGN, wn = wave % K::WGN;
   const float f = p.scale ? p.scale[1] : 1.0f;
   E* dw = static_cast<E*>(sh.dw[r]) + (uint64_t)sh.row0[r] * p.dim;
+  const RowStage<K, K::WM * 2, K::WN> stage(lds_address(lds), wave, lane);
+  if constexpr (ES == 2) __syncthreads();
 #pragma unroll
   for (int j = 0; j < K::NF; ++j) {
     const uint32_t v = row + wn * K::WN + j * 16 + (lane & 15);
 #pragma unroll
     for (int i = 0; i < K::MF; ++i) {
       const uint32_t d = col + wm * K::WM + i * 16 + 4 * (lane >> 4);
-      if (v >= sh.rows[r] || d >= p.dim) continue;
       E4 out;
 #pragma unroll
       for (int e = 0; e < 4; ++e) out[e] = (E)(acc[i][j][e] * f);
-      *reinterpret_cast<E4*>(dw + (uint64_t)v * p.dim + d) = out;
+      if constexpr (ES == 2) stage.put(j * 16 + (lane & 15), (i * 16 + 4 * (lane >> 4)) * 2, out);
+      else if (v < sh.rows[r] && d < p.dim) *reinterpret_cast<E4*>(dw + (uint64_t)v * p.dim + d) = out;
     }
   }
+  if constexpr (ES == 2)
+    stage.store(reinterpret_cast<char*>(dw + (uint64_t)(row + wn * K::WN) * p.dim + col + wm * K::WM), (uint64_t)p.dim * ES,
+                (int)(sh.rows[r] - row) - wn * K::WN, ((int)(p.dim - col) - wm * K::WM) * ES);
 }
 
 // --- tile shapes -------------------------------------------------------------
