@@ -266,35 +266,73 @@ __global__ __launch_bounds__(K::threads) void ortho_sym_join(OrthoMat q, char* w
   sym_store<K, PAIR, KIND>(q, ws + blockIdx.y * q.bytes, ti, tj, ca, cb, cc, acc);
 }
 
-// A tile's results, v[i][j] as in TileMma, as pairs into rows of a state matrix:
-// rows j along the columns i (origin: the tile's first row and column).  `width`
-// columns are left from the tile's first one (whole vectors), `rows` rows.
-template <class K>
-__device__ __forceinline__ void store_pairs(uint32_t lds, const typename K::Acc& v, char* origin, uint32_t pitch, int rows, int width) {
+// A tile's results, v[i][j] as in TileMma, into rows of a state matrix: rows j
+// along the columns i (origin: the tile's first row and column).  `width`
+// columns are left from the tile's first one (whole vectors), `rows` rows.  A
+// wave's share of LDS holds half of its pairs, or all of its hi or lo parts.
+template <class K, bool PAIR>
+__device__ __forceinline__ void store_tile(uint32_t lds, typename K::Acc& v, char* origin, char* lo_origin, uint32_t pitch,
+                                           int rows, int width) {
   const int lane = threadIdx.x & 63, wave = uniform(threadIdx.x >> 6), wm = wave / K::WGN, wn = wave % K::WGN;
-  constexpr int JP = K::NF / 2;          // the wave's share of LDS holds half of its pairs
-  const RowStage<K, K::WM * 4, JP * 16> stage(lds, wave, lane);
-  __syncthreads();
+  constexpr int size = PAIR ? 4 : 2, JP = PAIR ? K::NF / 2 : K::NF;
+  const RowStage<K, K::WM * size, JP * 16> stage(lds, wave, lane);
+  __syncthreads();                       // every wave is done with the product
 #pragma unroll
-  for (int q = 0; q < 2; ++q) {
+  for (int q = 0; q < 2; ++q) {          // half by half, or hi, then lo
+    const int j0 = PAIR ? q * JP : 0;
 #pragma unroll
     for (int j = 0; j < JP; ++j)
 #pragma unroll
       for (int i = 0; i < K::MF; ++i) {
+        // split anew for lo: kept since the hi pass, the lo parts would spill
+        if (!PAIR) asm volatile("" : "+v"(v[i][j]));
         f16x4 hi, lo;
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
           _Float16 h, l;
-          split(v[i][q * JP + j][e], h, l);
+          split(v[i][j0 + j][e], h, l);
           hi[e] = h;
           lo[e] = l;
         }
-        const uint32_t at = column<true>(i * 16 + 4 * (lane >> 4));
-        stage.put(j * 16 + (lane & 15), at, hi);
-        stage.put(j * 16 + (lane & 15), at + 64, lo);
+        const uint32_t at = column<PAIR>(i * 16 + 4 * (lane >> 4));
+        stage.put(j * 16 + (lane & 15), at, PAIR || q == 0 ? hi : lo);
+        if (PAIR) stage.put(j * 16 + (lane & 15), at + 64, lo);
       }
-    const int row = wn * K::WN + q * JP * 16;
-    stage.store(origin + (uint64_t)row * pitch + wm * K::WM * 4, pitch, rows - row, (width - wm * K::WM) * 4);
+    const int row = wn * K::WN + j0 * 16;
+    stage.store((PAIR || q == 0 ? origin : lo_origin) + (uint64_t)row * pitch + wm * K::WM * size, pitch, rows - row,
+                (width - wm * K::WM) * size);
+  }
+}
+
+// The same into rows of the result (whole 16-byte vectors, `ld` elements
+// apart; origin, rows and width in the result's orientation), or, for a tall
+// matrix, its transpose.
+template <class K, class E, bool TALL>
+__device__ __forceinline__ void store_result(uint32_t lds, const typename K::Acc& v, E* origin, uint32_t ld, int rows, int width) {
+  typedef E E4 __attribute__((ext_vector_type(4)));
+  const int lane = threadIdx.x & 63, wave = uniform(threadIdx.x >> 6), wm = wave / K::WGN, wn = wave % K::WGN;
+  constexpr int size = sizeof(E), passes = size / 2;
+  constexpr int IP = TALL ? K::MF / passes : K::MF, JP = TALL ? K::NF : K::NF / passes;
+  const RowStage<K, (TALL ? K::WN : K::WM) * size, (TALL ? IP : JP) * 16> stage(lds, wave, lane);
+  __syncthreads();
+#pragma unroll
+  for (int q = 0; q < passes; ++q) {
+#pragma unroll
+    for (int j = 0; j < JP; ++j)
+#pragma unroll
+      for (int i = 0; i < IP; ++i) {
+        const f32x4 x = v[TALL ? q * IP + i : i][TALL ? j : q * JP + j] * kInvScale * kInvScale;
+        const int along = i * 16 + 4 * (lane >> 4), across = j * 16 + (lane & 15);
+        E4 out;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) out[e] = (E)x[e];
+        if (!TALL) stage.put(across, along * size, out);
+        else
+#pragma unroll
+          for (int e = 0; e < 4; ++e) stage.put(along + e, across * size, (E)out[e]);
+      }
+    const int row = TALL ? wm * K::WM + q * IP * 16 : wn * K::WN + q * JP * 16, col = TALL ? wn * K::WN : wm * K::WM;
+    stage.store(reinterpret_cast<char*>(origin + (uint64_t)row * ld + col), (uint64_t)ld * size, rows - row, (width - col) * size);
   }
 }
 
@@ -314,12 +352,23 @@ __global__ __launch_bounds__(K::threads) void ortho_step(OrthoArgs a, OrthoMat q
   typename K::Acc acc = {};
   const Operand x{base + q.x[cur] + (uint64_t)c0 * (PAIR ? 4 : 2), q.xp, (int)(q.n - c0)};
   const Operand b{base + q.b + (uint64_t)r0 * q.ap, q.ap, (int)(q.m - r0)};
-  K::run(x, b, q.m, lds_address(lds), acc);
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, wm = wave / K::WGN, wn = wave % K::WGN;
-  E* out = static_cast<E*>(a.out[mat]);
-  const bool tall = a.rows > a.cols;
   const uint32_t width = q.xp / (PAIR ? 4 : 2);
-  if constexpr (PAIR && !LAST) {
+  if constexpr (!PAIR) {
+#pragma unroll
+    for (int j = 0; j < K::NF; ++j) {
+      const uint64_t row = (uint64_t)min(r0 + wn * K::WN + j * 16 + (lane & 15), q.m - 1) * q.xp;
+#pragma unroll
+      for (int i = 0; i < K::MF; ++i) {
+        float old[4];
+        get<PAIR>(base + q.x[cur] + row, base + q.lo[cur] + row, min(c0 + wm * K::WM + i * 16 + 4 * (lane >> 4), width - 4), old);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) acc[i][j][e] = ca * kScale * old[e];
+      }
+    }
+  }
+  K::run(x, b, q.m, lds_address(lds), acc);
+  if constexpr (!LAST) {
 #pragma unroll
     for (int i = 0; i < K::MF; ++i)
 #pragma unroll
@@ -327,37 +376,28 @@ __global__ __launch_bounds__(K::threads) void ortho_step(OrthoArgs a, OrthoMat q
 #pragma unroll
         for (int e = 0; e < 4; ++e)
           acc[i][j][e] = c0 + wm * K::WM + i * 16 + 4 * (lane >> 4) + e < q.n ? acc[i][j][e] * kInvScale : 0.0f;
-    store_pairs<K>(lds_address(lds), acc, base + q.x[cur ^ 1] + (uint64_t)r0 * q.xp + c0 * 4, q.xp, (int)(q.m - r0), (int)(width - c0));
-    return;
-  }
-#pragma unroll
-  for (int j = 0; j < K::NF; ++j) {
-    const uint32_t r = r0 + wn * K::WN + j * 16 + (lane & 15);
-    const uint64_t row = (uint64_t)min(r, q.m - 1) * q.xp;
-    float old[K::MF][4];
-    if (!PAIR) {                         // all reads before the first store, which could alias them
-#pragma unroll
-      for (int i = 0; i < K::MF; ++i) {
-        const uint32_t c = min(c0 + wm * K::WM + i * 16 + 4 * (lane >> 4), width - 4);
-        get<PAIR>(base + q.x[cur] + row, base + q.lo[cur] + row, c, old[i]);
-      }
+    const uint64_t tile = (uint64_t)r0 * q.xp + c0 * (PAIR ? 4 : 2);
+    store_tile<K, PAIR>(lds_address(lds), acc, base + q.x[cur ^ 1] + tile, base + q.lo[cur ^ 1] + tile, q.xp, (int)(q.m - r0),
+                        (int)(width - c0));
+  } else {
+    E* out = static_cast<E*>(a.out[mat]);
+    const bool tall = a.rows > a.cols;
+    if (a.cols % (16 / sizeof(E)) == 0) {
+      const int rows = (int)(q.m - r0), cols = (int)(q.n - c0);
+      if (tall) store_result<K, E, true>(lds_address(lds), acc, out + (uint64_t)c0 * a.cols + r0, a.cols, cols, rows);
+      else store_result<K, E, false>(lds_address(lds), acc, out + (uint64_t)r0 * a.cols + c0, a.cols, rows, cols);
+      return;
     }
 #pragma unroll
-    for (int i = 0; i < K::MF; ++i) {
-      const uint32_t c = c0 + wm * K::WM + i * 16 + 4 * (lane >> 4);
-      if (r >= q.m || c >= width) continue;
-      float v[4];
+    for (int j = 0; j < K::NF; ++j) {
+      const uint32_t r = r0 + wn * K::WN + j * 16 + (lane & 15);
 #pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        v[e] = (PAIR ? 0.0f : ca * old[i][e]) + acc[i][j][e] * kInvScale;
-        if (c + e >= q.n) v[e] = 0.0f;
-      }
-      if constexpr (LAST) {
+      for (int i = 0; i < K::MF; ++i) {
+        const uint32_t c = c0 + wm * K::WM + i * 16 + 4 * (lane >> 4);
 #pragma unroll
         for (int e = 0; e < 4; ++e)
-          if (c + e < q.n) out[tall ? (uint64_t)(c + e) * a.cols + r : (uint64_t)r * a.cols + c + e] = (E)(v[e] * kInvScale);
-      } else {
-        put<PAIR>(base + q.x[cur ^ 1] + row, base + q.lo[cur ^ 1] + row, c, v);
+          if (r < q.m && c + e < q.n)
+            out[tall ? (uint64_t)(c + e) * a.cols + r : (uint64_t)r * a.cols + c + e] = (E)(acc[i][j][e] * kInvScale * kInvScale);
       }
     }
   }
@@ -366,7 +406,7 @@ __global__ __launch_bounds__(K::threads) void ortho_step(OrthoArgs a, OrthoMat q
 template <bool PAIR, OperandKind A>
 using Big = TileMma<DType::F16, 256, 256, 2, 4, A, kRows, PAIR>;
 template <bool PAIR, OperandKind A>
-using Mid = TileMma<DType::F16, 128, 128, 2, 2, A, kRows, PAIR>;
+using Mid = TileMma<DType::F16, 128, 128, 2, 4, A, kRows, PAIR>;
 // one of these, alone on its CU, hides the loads behind three stages of them
 template <bool PAIR, OperandKind A>
 using Deep = TileMma<DType::F16, 128, 128, 2, 4, A, kRows, PAIR, 4>;
