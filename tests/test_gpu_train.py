@@ -117,6 +117,13 @@ def test_cross_entropy_and_gradient(vocab, tokens, dim, dtype):
     assert ok() and torch.equal(only, dx) and all(torch.equal(a, b) for a, b in zip(alone, dws))
 
 
+# sizes at which each of the three products takes the larger tiles
+@pytest.mark.parametrize("dtype", ["f32", "f16", "bf16"])
+@pytest.mark.parametrize("vocab,tokens,dim", [([4100, 4130], 1000, 1024), ([700, 330], 1024, 16384)])
+def test_cross_entropy_in_large_tiles(vocab, tokens, dim, dtype):
+    test_cross_entropy_and_gradient(vocab, tokens, dim, dtype)
+
+
 @pytest.mark.parametrize("dtype", ["f32", "f16", "bf16"])
 def test_cross_entropy_gradient_against_differences_of_its_own_loss(dtype):
     from double_binary_tree_amd import emucomm as E
@@ -385,6 +392,32 @@ def test_orthogonalize(n, rows, cols, dtype):
     E.orthogonalize_tensors(sends, sends)                     # in place, the same bits
     torch.cuda.synchronize()
     assert all(torch.equal(a, b) for a, b in zip(sends, recvs))
+
+
+# Many matrices, so that every tile shape is taken (the square products' and the
+# step's), wide and tall, with rows of whole 16-byte vectors and without; long
+# ones, whose products are split along the sum.
+ORTHO_MANY = [(64, 130, 200), (64, 200, 300), (64, 300, 296), (64, 304, 296), (64, 296, 301), (64, 521, 520), (40, 40, 5504),
+              (40, 5501, 40), (40, 24, 16400)]
+
+
+@pytest.mark.parametrize("dtype", ["f32", "f16", "bf16"])
+@pytest.mark.parametrize("n,rows,cols", ORTHO_MANY)
+def test_orthogonalize_many(n, rows, cols, dtype):
+    from double_binary_tree_amd import emucomm as E
+    announce(f"orthogonalize many, {n} x {rows} x {cols} {dtype}")
+    first = ortho_case(3, rows, cols, dtype)
+    sends = first + [first[i % 3].clone() for i in range(3, n)]
+    pairs = [guarded((rows, cols), sends[0].dtype) for _ in range(n)]
+    recvs = [p[0] for p in pairs]
+    size = E.orthogonalize_workspace(sends).numel()
+    whole = torch.full((size + 4096,), 0x5C, dtype=torch.uint8, device="cuda")
+    E.orthogonalize_tensors(sends, recvs, workspace=whole[:size])
+    torch.cuda.synchronize()
+    assert all(p[1]() for p in pairs) and bool((whole[size:] == 0x5C).all())
+    check_ortho(first, recvs[:3], 5, None, dtype)
+    # the same matrix gives the same bits, whatever its place
+    assert all(torch.equal(recvs[i], recvs[i % 3]) for i in range(3, n))
 
 
 @pytest.mark.parametrize("dtype", ["f32", "bf16"])
