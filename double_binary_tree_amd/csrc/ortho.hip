@@ -404,7 +404,7 @@ __global__ __launch_bounds__(K::threads) void ortho_step(OrthoArgs a, OrthoMat q
 }
 
 template <bool PAIR, OperandKind A>
-using Big = TileMma<DType::F16, 256, 256, 2, 4, A, kRows, PAIR>;
+using Big = TileMma<DType::F16, 256, 256, 2, 4, A, kRows, PAIR, PAIR ? 2 : 4, !PAIR>;
 template <bool PAIR, OperandKind A>
 using Mid = TileMma<DType::F16, 128, 128, 2, 4, A, kRows, PAIR>;
 // one of these, alone on its CU, hides the loads behind three stages of them

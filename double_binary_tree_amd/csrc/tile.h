@@ -4,22 +4,43 @@
 // of one k are contiguous); nothing is transposed in memory.
 //
 // Staging.  One k-step covers 128 bytes of k per row (64 16-bit or 32 f32
-// values), so a stage holds 128 bytes times BM + BN whatever the layout.  It
-// goes from global memory straight to LDS, 16 bytes a lane, 1 KiB a wave
-// access; STAGES stages rotate, so the loads of the STAGES - 1 steps after s run
-// while step s is multiplied.  LDS is filled in lane order, so the permutations below are
-// applied to the global addresses.
+// values; 64 bytes in the shifted schedule below), so a stage holds that times
+// BM + BN whatever the layout.  It goes from global memory straight to LDS, 16
+// bytes a lane, 1 KiB a wave access; STAGES stages rotate, so the loads of the
+// STAGES - 1 steps after s run while step s is multiplied.  LDS is filled in
+// lane order, so the permutations below are applied to the global addresses.
 //   kRows: a wave access holds 8 rows of 128 bytes.  The 16-byte chunk c of
 //     row r sits at chunk c ^ ((r >> 1) & 7): the 16 rows that a matrix
 //     instruction reads at one chunk then cover all 64 banks once (a row
 //     spans 32 banks, so rows r and r + 1 differ in the half, rows r and r + 2
-//     in the chunk).
+//     in the chunk).  Or 16 rows of 64 bytes, chunk c at c ^ p((r >> 2) & 3),
+//     p = 2, 0, 1, 3: a row spans 16 banks, four rows differ in the quarter,
+//     rows r and r + 4 in the chunk, and rows 0 - 3 and 12 - 15 at one chunk
+//     meet no bank of rows 4 - 11 at the next, which a 16-byte read takes
+//     together (with p the identity it took twice the LDS cycles).
 //   kCols: a stage holds the step's k, each with the tile's m side by side.
 //     16-bit fragments come through the LDS transpose read: of 16 lanes, lanes
 //     4j .. 4j + 3 read the 16 m (32 bytes) of one k, and lane i receives the
 //     four k of m = i.  A 32-byte window w of k-row r sits at window w ^ h(r),
 //     h taken so that the 8 windows that 32 lanes read together (k-rows j and
 //     8 + j, j = 0 .. 3) cover all banks once.
+//
+// Schedules.  Plain: every wave reads a step's fragments and multiplies them as
+// they come; two or more waves on a SIMD (or two workgroups on a CU) overlap
+// by drifting apart, and one barrier a step keeps the stages in order.
+// Shifted (SHIFT, eight waves, 64-byte steps, four stages): a step is a memory
+// phase (read the fragments, start the loads of step s + 3, wait for those of
+// s + 1) and a multiply phase; of the two waves on each SIMD the second runs
+// one phase behind, kept there by one barrier more at its start and a barrier
+// after every phase, so one wave's multiply phase is the other's memory phase
+// and the matrix cores do not wait for LDS.
+// Rates at 8192 x 8192 x 8192 in bf16, 256 x 256 tiles, kRows kRows / kCols
+// kRows / kCols kCols: plain 1288 / 1228 / 1212 TFLOP/s, shifted 1315 / 1314 /
+// 1268 (a library product of these sizes 1210 to 1540, by the clock that the
+// card's power leaves it).  128 x 128 tiles, two workgroups to a CU: plain 1123
+// / 1034 / 1044, shifted 918 / 1024 / 1073.  Pairs: plain 3 x 445, shifted the
+// same, so they keep the plain one.  The 32 x 32 x 16 instructions read less
+// LDS but draw more power: 1006 to 1230.
 //
 // Pairs (PAIR).  Numbers held as the sum of two f16, hi + lo, lie in blocks of
 // 32: 64 bytes of hi, then 64 bytes of lo.  A step then covers 32 k, and its
@@ -36,8 +57,6 @@
 #include "device_ops.h"
 
 namespace emu {
-
-constexpr int kStepBytes = 128;   // bytes of k per stage and row
 
 // What a matrix instruction multiplies: 16 bytes of a row per lane.
 template <DType T>
@@ -107,12 +126,13 @@ __device__ __forceinline__ i16x4 lds_read_transposed(uint32_t at) {
   return __builtin_amdgcn_ds_read_tr16_b64_v4i16((LdsQuad*)(uintptr_t)at);
 }
 
-// One operand's part of a stage: BX of m, `waves` waves loading it.
-template <DType T, int BX, OperandKind KIND, bool PAIR, int WAVES>
+// One operand's part of a stage: BX of m, STEP bytes of k per row, `waves` waves
+// loading it.
+template <DType T, int BX, OperandKind KIND, bool PAIR, int WAVES, int STEP>
 struct Side {
   static constexpr int es = T == DType::F32 ? 4 : 2;
-  static constexpr int kstep = PAIR ? 32 : kStepBytes / es;         // k per step
-  static constexpr int bytes = BX * kStepBytes;
+  static constexpr int kstep = PAIR ? 32 : STEP / es;         // k per step
+  static constexpr int bytes = BX * STEP;
   static constexpr int row_bytes = BX * (PAIR ? 4 : es);            // kCols: one k in LDS
   static constexpr int loads = bytes / 1024 / WAVES;                // per wave and stage
   static_assert(loads * 1024 * WAVES == bytes, "whole wave accesses");
@@ -120,6 +140,15 @@ struct Side {
   static_assert(KIND == kRows || row_bytes <= 1024, "a k-row within a wave access");
   static_assert(KIND == kRows || row_bytes >= 128, "four windows at least");
 
+  static constexpr int chunks_per_row = STEP / 16;
+  static_assert(STEP == 128 || (STEP == 64 && !PAIR), "bytes of k per row");
+
+  // What the chunks of row r are permuted by.
+  static __device__ __forceinline__ uint32_t mix(uint32_t r) {
+    if constexpr (STEP == 128) return (r >> 1) & 7;
+    const uint32_t q = (r >> 2) & 3;
+    return q >> 1 | (~(q ^ q >> 1) & 1) << 1;
+  }
   // Where window w of k-row r sits.
   static __device__ __forceinline__ uint32_t window(uint32_t w, uint32_t r) {
     if constexpr (row_bytes >= 256) return w ^ ((r & 3) | ((r >> 1) & 4));
@@ -130,8 +159,9 @@ struct Side {
   // with `left` k in the step; returns whether the place lies past them.
   static __device__ __forceinline__ bool place(const Operand& o, int wave, int lane, int l, int left, uint32_t& off) {
     if constexpr (KIND == kRows) {
-      const int r = (wave * loads + l) * 8 + (lane >> 3), c = (lane & 7) ^ ((r >> 1) & 7);
-      const int chunks = PAIR ? 8 : min(8, (left * es + 15) / 16);
+      const int r = (wave * loads + l) * (1024 / STEP) + lane / chunks_per_row;
+      const int c = lane % chunks_per_row ^ (int)mix((uint32_t)r);
+      const int chunks = PAIR ? chunks_per_row : min(chunks_per_row, (left * es + 15) / 16);
       off = (uint32_t)min(r, o.rows - 1) * o.ld + 16u * (uint32_t)min(c, chunks - 1);
       return c >= chunks;
     } else {
@@ -143,7 +173,7 @@ struct Side {
     }
   }
   static __device__ __forceinline__ uint64_t advance(const Operand& o) {
-    return KIND == kRows ? (uint64_t)kStepBytes : (uint64_t)kstep * o.ld;
+    return KIND == kRows ? (uint64_t)STEP : (uint64_t)kstep * o.ld;
   }
 
   // Addresses of fragment f (16 m) within the stage's part, before the stage's
@@ -153,8 +183,8 @@ struct Side {
     __device__ __forceinline__ Frag(int lane) {
       const uint32_t i = lane & 15, g = lane >> 4;
       if constexpr (KIND == kRows) {
-        base = i * kStepBytes;
-        h = (i >> 1) & 7;
+        base = i * STEP;
+        h = mix(i);
       } else if constexpr (es == 2) {
         const uint32_t r = 8 * g + (i >> 2);
         base = r * row_bytes + (i & 3) * 8;
@@ -167,7 +197,7 @@ struct Side {
     // kk: half of the step (16-bit: k 32 kk .. 32 kk + 31; f32: 16 kk ..; pairs: 0 hi, 1 lo)
     __device__ __forceinline__ u32x4 read(uint32_t part, uint32_t f, int kk, int lane) const {
       if constexpr (KIND == kRows) {
-        return lds_read(part + f * 16 * kStepBytes + base + (((uint32_t)kk * 4 + (lane >> 4)) ^ h) * 16);
+        return lds_read(part + f * 16 * STEP + base + (((uint32_t)kk * 4 + (lane >> 4)) ^ h) * 16);
       } else if constexpr (es == 2) {
         const uint32_t w = PAIR ? (f >> 1) * 4 + (f & 1) + 2 * kk : f;
         const uint32_t at = part + base + (w ^ h) * 32 + (PAIR ? 0 : kk * 32 * row_bytes);
@@ -191,13 +221,15 @@ struct Side {
 // acc[i][j] of a lane holds C[m][n] at m = 16 i + 4 (lane >> 4) + e, n = 16 j
 // + (lane & 15) of the wave's part, e = 0 .. 3.
 template <DType T, int BM_, int BN_, int WGM_, int WGN_, OperandKind KA = kRows, OperandKind KB = kRows, bool PAIR = false,
-          int STAGES = 2>
+          int STAGES = 2, bool SHIFT = false>
 struct TileMma {
   static constexpr int BM = BM_, BN = BN_, WGM = WGM_, WGN = WGN_;
   static constexpr int waves = WGM * WGN, threads = 64 * waves;
   static constexpr int WM = BM / WGM, WN = BN / WGN, MF = WM / 16, NF = WN / 16;
-  typedef Side<T, BM, KA, PAIR, waves> SA;
-  typedef Side<T, BN, KB, PAIR, waves> SB;
+  static constexpr int step = SHIFT ? 64 : 128;
+  static_assert(!SHIFT || (waves == 8 && STAGES == 4 && !PAIR), "the shifted schedule");
+  typedef Side<T, BM, KA, PAIR, waves, step> SA;
+  typedef Side<T, BN, KB, PAIR, waves, step> SB;
   static constexpr int kstep = SA::kstep;
   static constexpr int stage_bytes = SA::bytes + SB::bytes;
   static constexpr int lds_bytes = STAGES * stage_bytes;
@@ -240,6 +272,22 @@ struct TileMma {
     }
   }
 
+  // The two phases of the shifted schedule.
+  struct Frags { u32x4 a[MF], b[NF]; };
+  static __device__ __forceinline__ void read(uint32_t lds, int wm, int wn, int lane, const typename SA::Frag& pa,
+                                              const typename SB::Frag& pb, Frags& f) {
+#pragma unroll
+    for (int j = 0; j < NF; ++j) f.b[j] = pb.read(lds + SA::bytes, wn * NF + j, 0, lane);
+#pragma unroll
+    for (int i = 0; i < MF; ++i) f.a[i] = pa.read(lds, wm * MF + i, 0, lane);
+  }
+  static __device__ __forceinline__ void multiply(const Frags& f, Acc& acc) {
+#pragma unroll
+    for (int i = 0; i < MF; ++i)
+#pragma unroll
+      for (int j = 0; j < NF; ++j) Mma<T>::mul(f.a[i], f.b[j], acc[i][j]);
+  }
+
   // Adds the product over `k` (> 0) to acc.  On return every wave may still be
   // reading `lds`.
   static __device__ __forceinline__ void run(Operand a, Operand b, uint32_t k, uint32_t lds, Acc& acc) {
@@ -274,28 +322,62 @@ struct TileMma {
       a.base += da;
       b.base += db;
     };
+    // Zeros past k in the last step's stage, by the lanes that loaded there.
+    auto clear = [&](uint32_t s) {
+      const uint32_t at = lds + s % STAGES * stage_bytes;
+      const u32x4 zero = {0, 0, 0, 0};
+      uint32_t unused;
+#pragma unroll
+      for (int l = 0; l < SA::loads; ++l)
+        if (SA::place(a, wave, lane, l, left, unused)) lds_write(at + (wave * SA::loads + l) * 1024 + lane * 16, zero);
+#pragma unroll
+      for (int l = 0; l < SB::loads; ++l)
+        if (SB::place(b, wave, lane, l, left, unused))
+          lds_write(at + SA::bytes + (wave * SB::loads + l) * 1024 + lane * 16, zero);
+    };
 #pragma unroll
     for (uint32_t s = 0; s < STAGES - 1; ++s)
       if (s < steps) fetch(s);
-    for (uint32_t s = 0; s < steps; ++s) {
-      if (s + STAGES <= steps + 1) lds_arrived<(STAGES - 2) * loads>();
+    if constexpr (SHIFT) {
+      if (steps >= 3) lds_arrived<2 * loads>();
       else lds_arrived<0>();
-      __syncthreads();     // step s is in LDS; every wave is done with the stage of s - 1
-      const uint32_t at = lds + s % STAGES * stage_bytes;
-      if (s + STAGES - 1 < steps) fetch(s + STAGES - 1);
-      if (s + 1 == steps && left != kstep) {
-        const u32x4 zero = {0, 0, 0, 0};
-        uint32_t unused;
-#pragma unroll
-        for (int l = 0; l < SA::loads; ++l)
-          if (SA::place(a, wave, lane, l, left, unused)) lds_write(at + (wave * SA::loads + l) * 1024 + lane * 16, zero);
-#pragma unroll
-        for (int l = 0; l < SB::loads; ++l)
-          if (SB::place(b, wave, lane, l, left, unused))
-            lds_write(at + SA::bytes + (wave * SB::loads + l) * 1024 + lane * 16, zero);
+      if (steps == 1 && left != kstep) clear(0);
+      __syncthreads();                                      // step 0 is in LDS
+      const bool behind = wave >= waves / 2;
+      if (behind) __syncthreads();
+      for (uint32_t s = 0; s < steps; ++s) {
+        Frags f;
+        read(lds + s % STAGES * stage_bytes, wm, wn, lane, pa, pb, f);
+        if (s + 3 < steps) {
+          fetch(s + 3);                                     // where s - 1 was, which every wave has read
+          lds_arrived<2 * loads>();                         // of s + 1
+        } else if (s + 2 < steps) {
+          lds_arrived<loads>();
+        } else {
+          lds_arrived<0>();
+        }
+        if (s + 2 == steps && left != kstep) clear(s + 1);
+        __syncthreads();                                    // the fragments are here
+        __builtin_amdgcn_sched_barrier(0);
+        __builtin_amdgcn_s_setprio(1);
+        multiply(f, acc);
+        __builtin_amdgcn_s_setprio(0);
+        __builtin_amdgcn_sched_barrier(0);
         __syncthreads();
       }
-      multiply(at, wm, wn, lane, pa, pb, acc);
+      if (!behind) __syncthreads();
+    } else {
+      for (uint32_t s = 0; s < steps; ++s) {
+        if (s + STAGES <= steps + 1) lds_arrived<(STAGES - 2) * loads>();
+        else lds_arrived<0>();
+        __syncthreads();     // step s is in LDS; every wave is done with the stage of s - 1
+        if (s + STAGES - 1 < steps) fetch(s + STAGES - 1);
+        if (s + 1 == steps && left != kstep) {
+          clear(s);
+          __syncthreads();
+        }
+        multiply(lds + s % STAGES * stage_bytes, wm, wn, lane, pa, pb, acc);
+      }
     }
   }
 };

@@ -384,7 +384,7 @@ __global__ __launch_bounds__(K::threads) void xent_dw(Shards sh, DwTile p) {
 // --- tile shapes -------------------------------------------------------------
 
 template <DType T, OperandKind A = kRows, OperandKind B = kRows>
-using Big = TileMma<T, 256, 256, 2, 4, A, B>;
+using Big = TileMma<T, 256, 256, 2, 4, A, B, false, 4, true>;
 template <DType T, OperandKind A = kRows, OperandKind B = kRows>
 using Mid = TileMma<T, 128, 128, 2, 2, A, B>;
 template <DType T, OperandKind A = kRows, OperandKind B = kRows>
