@@ -407,9 +407,6 @@ template <bool PAIR, OperandKind A>
 using Big = TileMma<DType::F16, 256, 256, 2, 4, A, kRows, PAIR, PAIR ? 2 : 4, !PAIR>;
 template <bool PAIR, OperandKind A>
 using Mid = TileMma<DType::F16, 128, 128, 2, 4, A, kRows, PAIR>;
-// one of these, alone on its CU, hides the loads behind three stages of them
-template <bool PAIR, OperandKind A>
-using Deep = TileMma<DType::F16, 128, 128, 2, 4, A, kRows, PAIR, 4>;
 template <bool PAIR, OperandKind A>
 using Small = TileMma<DType::F16, 64, 64, 2, 2, A, kRows, PAIR>;
 
@@ -462,38 +459,41 @@ void launch_step(const OrthoArgs& a, const OrthoMat& q, char* ws, uint32_t cur, 
                        ca, tm, tn);
 }
 
-constexpr uint32_t kSplitWork = 16384;
-
 // The tiles of a product, and into how many shares its k is split.
-enum Shape { kBig, kMid, kDeep, kSmall };
+enum Shape { kBig, kMid, kSmall };
 struct Choice {
   Shape shape;
   uint32_t splits;
 };
-// The largest tile that still gives every CU one; 128 x 128 tiles are taken two
-// to a CU (kMid) or, if there are not that many, alone (kDeep).
+// The largest tile that still gives every CU one (128 x 128 tiles fit two to a
+// CU, 64 x 64 five).  256 x 256 against 128 x 128: 4 x 2048 x 2048 in f32 2.20
+// against 2.27 ms; 128 x 128 against 64 x 64 with 288 tiles for 256 CUs: 8 x
+// 1024 x 4096 in bf16 0.99 against 1.08 ms, and with 144 tiles (4 x 1024 x 1024
+// in f32) 0.50 against 0.42 ms.
 template <class F>
 Choice choose(int cus, uint32_t nmat, F tiles) {
   const uint64_t big = (uint64_t)tiles(256u) * nmat, mid = (uint64_t)tiles(128u) * nmat;
   if (big >= (uint64_t)cus) return {kBig, 1};
-  if (mid > (uint64_t)cus) return {kMid, 1};
-  return {2 * mid >= (uint64_t)cus ? kDeep : kSmall, 1};
+  return {mid > (uint64_t)cus ? kMid : kSmall, 1};
 }
 uint32_t triangle_tiles(uint32_t m, uint32_t b) {
   const uint32_t t = ceil_div(m, b);
   return t * (t + 1) / 2;
 }
 // A symmetric product over k.  Where 256 x 256 tiles are too few for the CUs,
-// their k is split so that about one round of workgroups fills them; that
-// takes a write and a read of the parts, so it needs a long k: at 2 x 2048 x
-// 8190 pairs 224 + 37 us against 335 us of 128 x 128 tiles, at 8 x 1024 x 4096
-// without pairs 53 + 26 us against 55 us.
+// their k is split in up to six shares so that about one round of workgroups
+// fills them.  The parts are written and read once more, so it takes a long k
+// and few shares: five steps on 2 x 2048 x 8190 in f32 (three shares) 3.21 ms,
+// 3.40 unsplit; 4 x 1024 x 8192 in f32 (six) 1.84 and 1.87; 1 x 2048 x 8192 in
+// f32 (seven) 1.76 and 1.72; 4 x 1024 x 4096 in f32 (six, shorter k) 1.10 and
+// 0.94; 2 x 2048 x 16384 in bf16 (three) 2.77 and 3.01.
+constexpr uint32_t kSplitWork = 16384;   // k times products
 Choice choose_sym(const OrthoMat& q, int cus, uint32_t nmat, uint32_t k, bool pairs) {
   const Choice c = choose(cus, nmat, [&](uint32_t b) { return triangle_tiles(q.m, b); });
   const uint64_t big = (uint64_t)triangle_tiles(q.m, 256) * nmat;
   if (c.shape == kBig || (uint64_t)k * (pairs ? 3 : 1) < kSplitWork) return c;
   const uint32_t splits = (uint32_t)((uint64_t)cus / big);
-  if (splits < 2 || splits > 8 || big * splits * 5 < (uint64_t)cus * 4) return c;
+  if (splits < 2 || splits > 6 || big * splits * 5 < (uint64_t)cus * 4) return c;
   return {kBig, splits};
 }
 
@@ -514,7 +514,6 @@ hipError_t run(const OrthoArgs& a, char* workspace, hipStream_t s) {
     switch (w.shape) {
       case kBig: launch_sym<Big<PAIR, kRows>, PAIR, KIND>(q, a.nranks, ws, parts, cur, w.splits, c, s); break;
       case kMid: launch_sym<Mid<PAIR, kRows>, PAIR, KIND>(q, a.nranks, ws, parts, cur, w.splits, c, s); break;
-      case kDeep: launch_sym<Deep<PAIR, kRows>, PAIR, KIND>(q, a.nranks, ws, parts, cur, w.splits, c, s); break;
       default: launch_sym<Small<PAIR, kRows>, PAIR, KIND>(q, a.nranks, ws, parts, cur, w.splits, c, s); break;
     }
   };
@@ -527,7 +526,6 @@ hipError_t run(const OrthoArgs& a, char* workspace, hipStream_t s) {
     switch (step.shape) {
       case kBig: launch_step<T, Big<PAIR, kCols>, PAIR>(a, q, ws, cur, c[0], last, s); break;
       case kMid: launch_step<T, Mid<PAIR, kCols>, PAIR>(a, q, ws, cur, c[0], last, s); break;
-      case kDeep: launch_step<T, Deep<PAIR, kCols>, PAIR>(a, q, ws, cur, c[0], last, s); break;
       default: launch_step<T, Small<PAIR, kCols>, PAIR>(a, q, ws, cur, c[0], last, s); break;
     }
   }
