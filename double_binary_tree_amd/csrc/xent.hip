@@ -390,18 +390,21 @@ using Mid = TileMma<T, 128, 128, 2, 2, A, B>;
 template <DType T, OperandKind A = kRows, OperandKind B = kRows>
 using Small = TileMma<T, 64, 64, 2, 2, A, B>;
 template <DType T, OperandKind A = kRows, OperandKind B = kRows>
-using Thin = TileMma<T, 128, 64, 4, 1, A, B, false, 3>;    // reads rows at 5.6 TB/s; two stages 5.1, four 5.4
+using Thin = TileMma<T, 128, 64, 4, 1, A, B, false, 3>;    // reads the rows at 5.6 TB/s; two stages 5.1, four 5.4
 
 uint32_t ceil_div(uint32_t a, uint32_t b) { return (a + b - 1) / b; }
 
-// The largest tile that still gives every CU a workgroup (128 x 128: two, as
-// they run two to a CU), for up to 64 tokens the one that is 64 wide.  At 301
-// tokens, 8009 rows, 520 wide in f32 the three products of a gradient take
-// 36 + 34 + 40 us with 64 x 64 tiles, 48 + 50 + 52 us with 128 x 128.
+// 256 x 256 tiles where they fill four fifths of the CUs, 128 x 128 where they
+// reach two per CU (they run two to a CU), 64 x 64 below; for up to 64 tokens
+// the tile that is 64 wide.  Losses of 4096 x 50257 x 2048 in f16 take 0.75 ms
+// with 256 x 256 tiles and 0.92 with 128 x 128; the gradient's products of 301 x
+// 8009 x 520 in f32 36 + 34 + 40 us with 64 x 64 and 48 + 50 + 52 with 128 x 128;
+// losses of 48 x 128003 x 4096 in bf16 188 us with the narrow tile and 201 with
+// 64 x 64 (of 48 x 32000 x 2048 in f32, bound by the f32 instructions, 92 and 85).
 enum Shape { kBig, kMid, kThin, kSmall };
 template <class F>
 Shape shape_of(uint32_t tokens, int cus, F tiles) {
-  if (tokens > 128 && tiles(256u) >= (uint64_t)cus) return kBig;
+  if (tokens > 128 && tiles(256u) * 5 >= (uint64_t)cus * 4) return kBig;
   if (tokens <= 64) return kThin;
   return tiles(128u) >= 2 * (uint64_t)cus ? kMid : kSmall;
 }
@@ -594,8 +597,13 @@ XentLossSpace xent_loss_space(const XentArgs& a, const Shards& all) {
   return m;
 }
 
-// A run takes as many positions as keep g within 2^28 values, at least 4096 (2^27: 3% slower at 8192 x 100277 x 4096); dx is split over the width of a run until its
-// tiles reach two per CU, at most 64 ways.
+// A run takes as many positions as keep g within 2^28 values, at least 4096
+// (2^27: 3% slower at 8192 x 100277 x 4096).  dx is split over the width of a
+// run: for 16-bit types in up to four shares, if its 256 x 256 tiles then fill
+// four fifths of the CUs; otherwise until its 128 x 128 tiles reach two per CU,
+// at most 64 ways.  Gradients of 4096 x 50000 x 2048 in bf16 take 2.20 ms in
+// two shares of large tiles, 2.42 in two of small ones; 2500 x 8000 x 2048 (240
+// tiles) 0.27 and 0.29; 2048 x 32000 x 2048 in f32 6.46 and 6.34.
 XentGradSpace xent_grad_space(const XentArgs& a, const Shards& all, bool dx, bool dw) {
   XentGradSpace m;
   const size_t es = (size_t)elem_size(a.type);
@@ -603,8 +611,12 @@ XentGradSpace xent_grad_space(const XentArgs& a, const Shards& all, bool dx, boo
   for (uint32_t r = 0; r < all.nranks; ++r) positions += align_up(all.rows[r], kShardAlign);
   m.width = (uint32_t)std::min<uint64_t>(positions, std::max<uint64_t>(4096, (((uint64_t)1 << 28) / a.tokens) / 256 * 256));
   m.vpitch = (uint32_t)align_up(m.width, 64);
-  const uint64_t tiles = (uint64_t)ceil_div(a.dim, 128) * ceil_div(a.tokens, 128);
-  while (m.splits < 64 && tiles * m.splits < 2 * (uint64_t)a.cus && m.width / (2 * m.splits) >= 256) m.splits *= 2;
+  const uint64_t tiles = (uint64_t)ceil_div(a.dim, 128) * ceil_div(a.tokens, 128), cus = a.cus;
+  const uint64_t big = (uint64_t)ceil_div(a.dim, 256) * ceil_div(a.tokens, 256);
+  const uint64_t shares = std::min<uint64_t>(4, std::max<uint64_t>(1, cus / big));
+  if (es == 2 && a.tokens > 128 && m.width / shares >= 256 && big * shares * 5 >= cus * 4) m.splits = (uint32_t)shares;
+  else
+    while (m.splits < 64 && tiles * m.splits < 2 * cus && m.width / (2 * m.splits) >= 256) m.splits *= 2;
   size_t at = 0;
   auto take = [&](size_t n) { const size_t p = at; at = align_up(at + n, 256); return p; };
   m.scale = take(2 * sizeof(float));

@@ -119,7 +119,7 @@ def test_cross_entropy_and_gradient(vocab, tokens, dim, dtype):
 
 # sizes at which each of the three products takes the larger tiles
 @pytest.mark.parametrize("dtype", ["f32", "f16", "bf16"])
-@pytest.mark.parametrize("vocab,tokens,dim", [([4100, 4130], 1000, 1024), ([700, 330], 1024, 16384)])
+@pytest.mark.parametrize("vocab,tokens,dim", [([4100, 4130], 1000, 1024), ([700, 330], 1024, 16384), ([700, 501], 1020, 4160)])
 def test_cross_entropy_in_large_tiles(vocab, tokens, dim, dtype):
     test_cross_entropy_and_gradient(vocab, tokens, dim, dtype)
 
