@@ -163,13 +163,11 @@ __device__ __forceinline__ void triangle(uint32_t t, uint32_t& i, uint32_t& j) {
 }
 
 // What a symmetric product does with its tile.  kGram: A = X X^T;
-// kPoly: B = b A + c A A, plus a on the diagonal with pairs (X' = (a + B) X
-// then needs no second look at X; without pairs a's product with X would lose
-// X's lo part).
+// kPoly: B = b A + c A A.
 enum SymKind { kGram, kPoly };
 
 template <class K, bool PAIR, SymKind KIND>
-__device__ __forceinline__ void sym_store(const OrthoMat& q, char* base, uint32_t ti, uint32_t tj, float ca, float cb, float cc,
+__device__ __forceinline__ void sym_store(const OrthoMat& q, char* base, uint32_t ti, uint32_t tj, float cb, float cc,
                                           typename K::Acc& acc) {
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, wm = wave / K::WGN, wn = wave % K::WGN;
   char* out = base + (KIND == kGram ? q.a : q.b);
@@ -194,7 +192,7 @@ __device__ __forceinline__ void sym_store(const OrthoMat& q, char* base, uint32_
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
         v[e] = acc[i][j][e] * kInvScale;
-        if (KIND == kPoly) v[e] = cb * old[i][e] + cc * v[e] + (PAIR && r + e == c ? ca * kScale : 0.0f);
+        if (KIND == kPoly) v[e] = cb * old[i][e] + cc * v[e];
         if (r + e >= q.m) v[e] = 0.0f;
       }
       put<PAIR>(out + (uint64_t)c * q.ap, nullptr, r, v);
@@ -218,7 +216,7 @@ __device__ __forceinline__ void sym_store(const OrthoMat& q, char* base, uint32_
 // ortho_sym_join adds.
 template <class K, bool PAIR, SymKind KIND>
 __global__ __launch_bounds__(K::threads) void ortho_sym(OrthoMat q, char* ws, float* parts, uint32_t cur, uint32_t tiles,
-                                                        uint32_t shares, uint32_t share, float ca, float cb, float cc) {
+                                                        uint32_t shares, uint32_t share, float cb, float cc) {
   __shared__ __attribute__((aligned(16))) char lds[K::lds_bytes];
   static_assert(K::BM == K::BN, "square tiles");
   uint32_t ti, tj;
@@ -241,13 +239,13 @@ __global__ __launch_bounds__(K::threads) void ortho_sym(OrthoMat q, char* ws, fl
       for (int j = 0; j < K::NF; ++j) to[(i * K::NF + j) * K::threads] = acc[i][j];
     return;
   }
-  sym_store<K, PAIR, KIND>(q, base, ti, tj, ca, cb, cc, acc);
+  sym_store<K, PAIR, KIND>(q, base, ti, tj, cb, cc, acc);
 }
 
 // The parts of a tile added in order, then as in ortho_sym.
 template <class K, bool PAIR, SymKind KIND>
 __global__ __launch_bounds__(K::threads) void ortho_sym_join(OrthoMat q, char* ws, const float* __restrict__ parts,
-                                                             uint32_t nparts, float ca, float cb, float cc) {
+                                                             uint32_t nparts, float cb, float cc) {
   uint32_t ti, tj;
   triangle(blockIdx.x, ti, tj);
   typename K::Acc acc;
@@ -263,7 +261,34 @@ __global__ __launch_bounds__(K::threads) void ortho_sym_join(OrthoMat q, char* w
     for (int i = 0; i < K::MF; ++i)
 #pragma unroll
       for (int j = 0; j < K::NF; ++j) acc[i][j] += from[z * step + (i * K::NF + j) * K::threads];
-  sym_store<K, PAIR, KIND>(q, ws + blockIdx.y * q.bytes, ti, tj, ca, cb, cc, acc);
+  sym_store<K, PAIR, KIND>(q, ws + blockIdx.y * q.bytes, ti, tj, cb, cc, acc);
+}
+
+// v[i][j] = v[i][j] / scale + a X, X's pairs read by rows (origin: the tile's
+// first row and column; `rows` and `width` as in store_tile, positive).
+template <class K>
+__device__ __forceinline__ void add_pairs(uint32_t lds, typename K::Acc& v, float ca, const char* origin, uint32_t pitch, int rows,
+                                          int width) {
+  const int lane = threadIdx.x & 63, wave = uniform(threadIdx.x >> 6), wm = wave / K::WGN, wn = wave % K::WGN;
+  constexpr int JP = K::NF / 2;          // a wave's share of LDS holds half of its pairs
+  const RowStage<K, K::WM * 4, JP * 16> stage(lds, wave, lane);
+  const int col = min(wm * K::WM, width - 32);       // a part outside the matrix reads some place inside
+  __syncthreads();                       // every wave is done with the product
+#pragma unroll
+  for (int q = 0; q < 2; ++q) {
+    const int row = min(wn * K::WN + q * JP * 16, rows - 1);
+    stage.load(origin + (uint64_t)row * pitch + col * 4, pitch, rows - row, (width - col) * 4);
+    lds_arrived<0>();
+#pragma unroll
+    for (int j = 0; j < JP; ++j)
+#pragma unroll
+      for (int i = 0; i < K::MF; ++i) {
+        const uint32_t at = column<true>(i * 16 + 4 * (lane >> 4));
+        const f16x4 hi = stage.template get<f16x4>(j * 16 + (lane & 15), at), lo = stage.template get<f16x4>(j * 16 + (lane & 15), at + 64);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) v[i][q * JP + j][e] = v[i][q * JP + j][e] * kInvScale + ca * ((float)hi[e] + (float)lo[e]);
+      }
+  }
 }
 
 // A tile's results, v[i][j] as in TileMma, into rows of a state matrix: rows j
@@ -321,7 +346,7 @@ __device__ __forceinline__ void store_result(uint32_t lds, const typename K::Acc
     for (int j = 0; j < JP; ++j)
 #pragma unroll
       for (int i = 0; i < IP; ++i) {
-        const f32x4 x = v[TALL ? q * IP + i : i][TALL ? j : q * JP + j] * kInvScale * kInvScale;
+        const f32x4 x = v[TALL ? q * IP + i : i][TALL ? j : q * JP + j] * kInvScale;
         const int along = i * 16 + 4 * (lane >> 4), across = j * 16 + (lane & 15);
         E4 out;
 #pragma unroll
@@ -337,8 +362,11 @@ __device__ __forceinline__ void store_result(uint32_t lds, const typename K::Acc
 }
 
 // X' = a X + B X into the other buffers, or, in the last step, into the
-// output (with pairs a is in B).  First operand X as columns of k, second B
-// (rows).
+// output.  First operand X as columns of k, second B (rows).  With pairs a X is
+// added at the end: sums that start with it (or a on B's diagonal) round every
+// addition at its size, which took the error of 8190 x 2048 in f32 from 5e-6 to
+// 1.1e-5.  Without pairs the sums do start with a X, 20 us less per step of 8 x
+// 1024 x 4096: there the factors' own rounding, 2^-12, is far larger.
 template <DType T, class K, bool PAIR, bool LAST>
 __global__ __launch_bounds__(K::threads) void ortho_step(OrthoArgs a, OrthoMat q, char* ws, uint32_t cur, float ca,
                                                          uint32_t tm, uint32_t tn) {
@@ -368,6 +396,15 @@ __global__ __launch_bounds__(K::threads) void ortho_step(OrthoArgs a, OrthoMat q
     }
   }
   K::run(x, b, q.m, lds_address(lds), acc);
+  const uint64_t tile = (uint64_t)r0 * q.xp + c0 * (PAIR ? 4 : 2);
+  if constexpr (PAIR) {
+    add_pairs<K>(lds_address(lds), acc, ca, base + q.x[cur] + tile, q.xp, (int)(q.m - r0), (int)(width - c0));
+  } else {
+#pragma unroll
+    for (int i = 0; i < K::MF; ++i)
+#pragma unroll
+      for (int j = 0; j < K::NF; ++j) acc[i][j] *= kInvScale;
+  }
   if constexpr (!LAST) {
 #pragma unroll
     for (int i = 0; i < K::MF; ++i)
@@ -375,8 +412,7 @@ __global__ __launch_bounds__(K::threads) void ortho_step(OrthoArgs a, OrthoMat q
       for (int j = 0; j < K::NF; ++j)
 #pragma unroll
         for (int e = 0; e < 4; ++e)
-          acc[i][j][e] = c0 + wm * K::WM + i * 16 + 4 * (lane >> 4) + e < q.n ? acc[i][j][e] * kInvScale : 0.0f;
-    const uint64_t tile = (uint64_t)r0 * q.xp + c0 * (PAIR ? 4 : 2);
+          if (c0 + wm * K::WM + i * 16 + 4 * (lane >> 4) + e >= q.n) acc[i][j][e] = 0.0f;
     store_tile<K, PAIR>(lds_address(lds), acc, base + q.x[cur ^ 1] + tile, base + q.lo[cur ^ 1] + tile, q.xp, (int)(q.m - r0),
                         (int)(width - c0));
   } else {
@@ -397,7 +433,7 @@ __global__ __launch_bounds__(K::threads) void ortho_step(OrthoArgs a, OrthoMat q
 #pragma unroll
         for (int e = 0; e < 4; ++e)
           if (r < q.m && c + e < q.n)
-            out[tall ? (uint64_t)(c + e) * a.cols + r : (uint64_t)r * a.cols + c + e] = (E)(acc[i][j][e] * kInvScale * kInvScale);
+            out[tall ? (uint64_t)(c + e) * a.cols + r : (uint64_t)r * a.cols + c + e] = (E)(acc[i][j][e] * kInvScale);
       }
     }
   }
@@ -443,10 +479,10 @@ void launch_sym(const OrthoMat& q, uint32_t nmat, char* ws, float* parts, uint32
   const uint32_t share = (uint32_t)align_up(ceil_div(k, splits), 64);
   const uint32_t tiles = t * (t + 1) / 2, shares = ceil_div(k, share);
   hipLaunchKernelGGL((ortho_sym<K, PAIR, KIND>), dim3(tiles * shares * nmat), dim3(K::threads), 0, s, q, ws, parts, cur,
-                     tiles, shares, share, c[0], c[1], c[2]);
+                     tiles, shares, share, c[1], c[2]);
   if (shares > 1)
     hipLaunchKernelGGL((ortho_sym_join<K, PAIR, KIND>), dim3(tiles, nmat), dim3(K::threads), 0, s, q, ws, parts, shares,
-                       c[0], c[1], c[2]);
+                       c[1], c[2]);
 }
 template <DType T, class K, bool PAIR>
 void launch_step(const OrthoArgs& a, const OrthoMat& q, char* ws, uint32_t cur, float ca, bool last, hipStream_t s) {
