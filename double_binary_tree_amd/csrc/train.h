@@ -46,9 +46,9 @@ struct XentLossSpace {
   size_t bytes = 0;
 };
 struct XentGradSpace {
-  size_t scale = 0;             // factor on the stored gradients, and its inverse
-  size_t x = 0;                 // x with zeros for tokens without a loss
-  size_t g = 0;                 // d loss / d logits of the run [tokens][vpitch]
+  size_t weight = 0;            // largest |dloss|, and the factor of dw
+  size_t x = 0;                 // x as dw multiplies it, zeros for tokens without a loss
+  size_t g = 0;                 // d loss / d logits of the run [tokens][vpitch], 16-bit types before dloss
   size_t part = 0;              // [splits][tokens][dim] f32 parts of dx
   size_t bytes = 0;
   uint32_t vpitch = 0;          // in elements

@@ -14,6 +14,14 @@
 // it: dx along its rows, dw along its columns.  dx is summed in f32 over the
 // runs and rounded once.
 //
+// 16-bit types store q_tv = exp(z_tv - lse_t) - [v = y(t)] in place of g (one
+// rounding), dloss_t is a factor of the finished dx, and dw = D q^T x' with
+// x'_t = (dloss_t / D) x_t, D = max |dloss|.  A token's largest entry is mostly
+// q_ty, near -1 and then nearly exact, and with equal weights, as in a mean, x'
+// is x.  With dloss_t in the stored g the rounding of that one entry was common
+// to a whole row of both gradients: for a dozen tokens dw in bf16 was off by
+// 3.3e-3 in norm, where rounding the result alone gives 1.7e-3.
+//
 // Vocabulary rows are the product's first operand (lanes hold 4 consecutive
 // rows of one token), so a token's maximum and sum are mostly within a lane.
 #include "tile.h"
@@ -157,11 +165,15 @@ __global__ __launch_bounds__(kJoinTokens* kJoinLanes) void xent_join(
   }
 }
 
-// f16 gradients are stored scaled by the power of two that brings the largest
-// |dloss| to [2^14, 2^15): |exp(z - lse) - 1| is at most 1 (for an lse of
-// these logits), and a probability of 2^-29 still keeps every bit.
-__global__ __launch_bounds__(1024) void xent_scale(const float* __restrict__ dloss, const int64_t* __restrict__ targets,
-                                                   uint32_t tokens, int64_t vocab, float* __restrict__ scale) {
+// f16 holds q times 2^14: |q| is at most 1 (for an lse of these logits), and a
+// probability of 2^-28 still keeps every bit.
+template <DType T>
+constexpr float kStored = T == DType::F16 ? 16384.0f : 1.0f;
+
+// weight[0] = D, the largest |dloss| of the tokens with a loss, weight[1] = D
+// over what q was multiplied by.
+__global__ __launch_bounds__(1024) void xent_weight(const float* __restrict__ dloss, const int64_t* __restrict__ targets,
+                                                    uint32_t tokens, int64_t vocab, float stored, float* __restrict__ weight) {
   __shared__ float part[16];
   float big = 0.0f;
   for (uint32_t t = threadIdx.x; t < tokens; t += 1024) {
@@ -174,23 +186,34 @@ __global__ __launch_bounds__(1024) void xent_scale(const float* __restrict__ dlo
   __syncthreads();
   if (threadIdx.x == 0) {
     for (int w = 1; w < 16; ++w) big = fmaxf(big, part[w]);
-    int e = 0;
-    (void)frexpf(big, &e);                                 // big = f 2^e, f in [1/2, 1)
-    e = big > 0.0f ? min(max(15 - e, -126), 126) : 0;
-    scale[0] = ldexpf(1.0f, e);
-    scale[1] = ldexpf(1.0f, -e);
+    weight[0] = big;
+    weight[1] = big / stored;
   }
 }
 
-// x with zeros in the rows of tokens without a loss: such a token then adds
-// nothing to dw, whatever its hidden state holds.
+// x (16-bit types: x') with zeros in the rows of tokens without a loss: such a
+// token then adds nothing to dw, whatever its hidden state holds.
+template <DType T>
 __global__ __launch_bounds__(256) void xent_clean(const u32x4* __restrict__ x, const int64_t* __restrict__ targets,
+                                                  const float* __restrict__ dloss, const float* __restrict__ weight,
                                                   uint64_t vecs, uint32_t per_token, int64_t vocab,
                                                   u32x4* __restrict__ out) {
+  typedef typename Elem<T>::type E;
+  typedef E EV __attribute__((ext_vector_type(16 / sizeof(E))));
   for (uint64_t i = (uint64_t)blockIdx.x * 256 + threadIdx.x; i < vecs; i += (uint64_t)gridDim.x * 256) {
-    const int64_t y = targets[i / per_token];
+    const uint64_t t = i / per_token;
+    const int64_t y = targets[t];
     u32x4 v = {0, 0, 0, 0};
-    if (y >= 0 && y < vocab) v = x[i];
+    if (y >= 0 && y < vocab) {
+      v = x[i];
+      if constexpr (sizeof(E) == 2) {
+        const float big = weight[0], f = big > 0.0f ? dloss[t] / big : 0.0f;
+        EV e = bits<EV>(v);
+#pragma unroll
+        for (int k = 0; k < 8; ++k) e[k] = (E)((float)e[k] * f);
+        v = bits<u32x4>(e);
+      }
+    }
     out[i] = v;
   }
 }
@@ -200,13 +223,12 @@ struct GradTile {
   const int64_t* targets;
   const float* lse;
   const float* dloss;
-  const float* scale;          // null: 1
   void* g;
   uint32_t tokens, dim, vpitch, tm, tn, band;
   int64_t vocab;
 };
 
-// g of the run's rows for every token.  Positions between a rank's last row
+// g (16-bit types: q) of the run's rows for every token.  Positions between a rank's last row
 // and the next multiple of kShardAlign become zeros: the products that read g
 // go over whole vectors.
 template <DType T, class K>
@@ -227,7 +249,6 @@ __global__ __launch_bounds__(K::threads) void xent_dlogits(Shards sh, GradTile p
   K::run(a, b, p.dim, lds_address(lds), acc);
 
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, wm = wave / K::WGN, wn = wave % K::WGN;
-  const float scale = p.scale ? p.scale[0] : 1.0f;
   const uint32_t first = sh.first[r] + row;
   E* g = static_cast<E*>(p.g);
   const RowStage<K, K::WM * 2, K::WN> stage(lds_address(lds), wave, lane);
@@ -239,7 +260,7 @@ __global__ __launch_bounds__(K::threads) void xent_dlogits(Shards sh, GradTile p
     const bool counted = id >= 0 && id < p.vocab;
     const int64_t at = id - (int64_t)sh.id0[r] - row;
     const int y = at >= 0 && at < rows ? (int)at : -1;
-    const float lse = p.lse[tt], d = p.dloss[tt] * scale;
+    const float lse = p.lse[tt], d = ES == 2 ? kStored<T> : p.dloss[tt];
 #pragma unroll
     for (int i = 0; i < K::MF; ++i) {
       const int v = wm * K::WM + i * 16 + 4 * (lane >> 4);
@@ -308,21 +329,22 @@ __global__ __launch_bounds__(K::threads) void xent_dx(Shards sh, DxTile p) {
   }
 }
 
-// dx = (sum of the parts, in order) * unscale, rounded once; zeros for a token
-// without a loss.  Four values a lane (dim is a multiple of 4).
+// dx = the sum of the parts, in order (16-bit types: times dloss), rounded once;
+// zeros for a token without a loss.  Four values a lane (dim is a multiple of 4).
 template <DType T>
 __global__ __launch_bounds__(256) void xent_dx_join(const float* __restrict__ part, uint32_t splits, uint64_t quads,
                                                     uint32_t per_token, const int64_t* __restrict__ targets,
-                                                    int64_t vocab, const float* __restrict__ scale,
+                                                    int64_t vocab, const float* __restrict__ dloss,
                                                     void* __restrict__ dx) {
   typedef typename Elem<T>::type E;
   typedef E E4 __attribute__((ext_vector_type(4)));
-  const float f = scale ? scale[1] : 1.0f;
   for (uint64_t q = (uint64_t)blockIdx.x * 256 + threadIdx.x; q < quads; q += (uint64_t)gridDim.x * 256) {
     f32x4 s = reinterpret_cast<const f32x4*>(part)[q];
     for (uint32_t i = 1; i < splits; ++i) s += reinterpret_cast<const f32x4*>(part)[i * quads + q];
-    const int64_t y = targets[q / per_token];
+    const uint64_t t = q / per_token;
+    const int64_t y = targets[t];
     const bool counted = y >= 0 && y < vocab;
+    const float f = sizeof(E) == 2 ? dloss[t] / kStored<T> : 1.0f;
     E4 out;
 #pragma unroll
     for (int e = 0; e < 4; ++e) out[e] = (E)(counted ? s[e] * f : 0.0f);
@@ -342,7 +364,7 @@ __global__ __launch_bounds__(256) void xent_zero(Shards sh, uint64_t row_bytes) 
 struct DwTile {
   const void* x;
   const void* g;
-  const float* scale;
+  const float* weight;         // 16-bit types
   uint32_t tokens, dim, vpitch, tm, tn, band;
 };
 template <DType T, class K>
@@ -359,7 +381,7 @@ __global__ __launch_bounds__(K::threads) void xent_dw(Shards sh, DwTile p) {
   typename K::Acc acc = {};
   K::run(a, b, p.tokens, lds_address(lds), acc);
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, wm = wave / K::WGN, wn = wave % K::WGN;
-  const float f = p.scale ? p.scale[1] : 1.0f;
+  const float f = ES == 2 ? p.weight[1] : 1.0f;
   E* dw = static_cast<E*>(sh.dw[r]) + (uint64_t)sh.row0[r] * p.dim;
   const RowStage<K, K::WM * 2, K::WN> stage(lds_address(lds), wave, lane);
   if constexpr (ES == 2) __syncthreads();
@@ -515,27 +537,23 @@ hipError_t grad_of(const XentArgs& a, const Shards& all, char* ws, hipStream_t s
   bool dw = false;
   for (uint32_t r = 0; r < all.nranks; ++r) dw = dw || all.dw[r] != nullptr;
   const XentGradSpace m = xent_grad_space(a, all, dx, dw);
-  const float* scale = nullptr;
+  float* weight = reinterpret_cast<float*>(ws + m.weight);
   int64_t vocab = 0;
   for (uint32_t r = 0; r < all.nranks; ++r) vocab += all.rows[r];
   hipError_t e;
-  if (T == DType::F16) {
-    hipLaunchKernelGGL(xent_scale, dim3(1), dim3(1024), 0, s, a.dloss, a.targets, a.tokens, vocab,
-                       reinterpret_cast<float*>(ws + m.scale));
-    scale = reinterpret_cast<const float*>(ws + m.scale);
-  }
   if (dw) {
+    if (ES == 2)
+      hipLaunchKernelGGL(xent_weight, dim3(1), dim3(1024), 0, s, a.dloss, a.targets, a.tokens, vocab, kStored<T>, weight);
     const uint64_t vecs = (uint64_t)a.tokens * a.dim * ES / kVecBytes;
-    hipLaunchKernelGGL(xent_clean, dim3((uint32_t)std::min<uint64_t>((vecs + 255) / 256, (uint64_t)a.cus * 16)), dim3(256),
-                       0, s, static_cast<const u32x4*>(a.x), a.targets, vecs, (uint32_t)(a.dim * ES / kVecBytes), vocab,
-                       reinterpret_cast<u32x4*>(ws + m.x));
+    hipLaunchKernelGGL(xent_clean<T>, dim3((uint32_t)std::min<uint64_t>((vecs + 255) / 256, (uint64_t)a.cus * 16)), dim3(256),
+                       0, s, static_cast<const u32x4*>(a.x), a.targets, a.dloss, weight, vecs,
+                       (uint32_t)(a.dim * ES / kVecBytes), vocab, reinterpret_cast<u32x4*>(ws + m.x));
   }
   GradTile gp{};
   gp.x = a.x;
   gp.targets = a.targets;
   gp.lse = a.lse;
   gp.dloss = a.dloss;
-  gp.scale = scale;
   gp.g = ws + m.g;
   gp.tokens = a.tokens;
   gp.dim = a.dim;
@@ -566,7 +584,7 @@ hipError_t grad_of(const XentArgs& a, const Shards& all, char* ws, hipStream_t s
       DwTile p{};
       p.x = ws + m.x;
       p.g = ws + m.g;
-      p.scale = scale;
+      p.weight = weight;
       p.tokens = a.tokens;
       p.dim = a.dim;
       p.vpitch = m.vpitch;
@@ -581,7 +599,7 @@ hipError_t grad_of(const XentArgs& a, const Shards& all, char* ws, hipStream_t s
     const uint64_t quads = (uint64_t)a.tokens * a.dim / 4;
     hipLaunchKernelGGL(xent_dx_join<T>, dim3((uint32_t)std::min<uint64_t>((quads + 255) / 256, (uint64_t)a.cus * 16)),
                        dim3(256), 0, s, reinterpret_cast<const float*>(ws + m.part), m.splits, quads,
-                       a.dim / 4, a.targets, vocab, scale, a.dx);
+                       a.dim / 4, a.targets, vocab, a.dloss, a.dx);
   }
   return hipGetLastError();
 }
@@ -619,7 +637,7 @@ XentGradSpace xent_grad_space(const XentArgs& a, const Shards& all, bool dx, boo
     while (m.splits < 64 && tiles * m.splits < 2 * cus && m.width / (2 * m.splits) >= 256) m.splits *= 2;
   size_t at = 0;
   auto take = [&](size_t n) { const size_t p = at; at = align_up(at + n, 256); return p; };
-  m.scale = take(2 * sizeof(float));
+  m.weight = take(2 * sizeof(float));
   m.g = take((size_t)a.tokens * m.vpitch * es);
   if (dw) m.x = take((size_t)a.tokens * a.dim * es);
   if (dx) m.part = take((size_t)m.splits * a.tokens * a.dim * sizeof(float));

@@ -231,8 +231,8 @@ def test_cross_entropy_gradient_in_several_runs():
     ok = y >= 0
     p[ok.nonzero()[:, 0], y[ok]] -= 1
     p *= (d.double() * ok)[:, None]
-    # rounding g and the result: at most 2^-8 each relative to the terms'
-    # magnitudes, in the 2-norm below 2^-8 (1 + 1) of the result's own
+    # rounding q, x' and the result: at most 2^-8 each relative to the terms'
+    # magnitudes, independent of one another, in the 2-norm below 2^-8 sqrt(3)
     for got, ref in zip([dx, *dws], [p @ w, *(p.t().contiguous() @ x.double()).split(vocab)]):
         assert float((got.double() - ref).norm() / ref.norm()) < 2 * 2.0 ** -8
 

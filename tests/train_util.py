@@ -72,13 +72,20 @@ def xent_bounds(x, ws, targets, lse, dloss, dtype):
     q = np.exp(np.minimum(z - lse[:, None], 80.0))
     dg = np.abs(dloss)[:, None] * q * (dz + (np.abs(z - lse[:, None]) + 4) * 4 * U32) + np.abs(g) * 4 * U32
     dg[~ok] = 0.0
-    # stored in the buffer type (f16: scaled so that its smallest step is 2^-24 / 2^14 of the largest |dloss|)
+    # stored in the buffer type: f32 as it is, 16-bit types as q = g / dloss
+    # (f16: times 2^14, so that its smallest step is 2^-24 / 2^14 of |dloss|)
     top = np.abs(dloss[ok]).max() if ok.any() else 0.0
-    dg += np.abs(g) * ROUND[dtype] + (top * 2.0 ** -38 if dtype == "f16" else TINY[dtype])
+    dg += np.abs(g) * ROUND[dtype] + (top * 2.0 ** -38 if dtype == "f16" else TINY[dtype] * max(1.0, top))
     dg[~ok] = 0.0
     xs = np.where(ok[:, None], np.abs(x), 0.0)
-    dx_tol = dg @ np.abs(w) + sum_bound(len(w)) * (np.abs(g) @ np.abs(w))
-    dw_tol = dg.T @ xs + sum_bound(len(x)) * (np.abs(g).T @ xs)
+    size_dx, size_dw = np.abs(g) @ np.abs(w), np.abs(g).T @ xs
+    # a 16-bit dx is multiplied by dloss (one rounding in f32)
+    dx_tol = dg @ np.abs(w) + (sum_bound(len(w)) + U32) * size_dx
+    dw_tol = dg.T @ xs + sum_bound(len(x)) * size_dw
+    if dtype != "f32":
+        # x' = x dloss / top: two roundings in f32, one to the type (half of its
+        # smallest step where that is more); dw is multiplied by top (over 2^14)
+        dw_tol += (ROUND[dtype] + 4 * U32) * size_dw + TINY[dtype] / 2 * top * q[ok].sum(0)[:, None] + TINY[dtype] * top * len(x)
     return loss_tol, lse_tol, dx_tol, dw_tol
 
 
