@@ -416,16 +416,21 @@ using Thin = TileMma<T, 128, 64, 4, 1, A, B, false, 3>;    // reads the rows at 
 
 uint32_t ceil_div(uint32_t a, uint32_t b) { return (a + b - 1) / b; }
 
-// 256 x 256 tiles where they fill four fifths of the CUs, 128 x 128 where they
-// reach two per CU (they run two to a CU), 64 x 64 below; for up to 64 tokens
-// the tile that is 64 wide.  Losses of 4096 x 50257 x 2048 in f16 take 0.75 ms
-// with 256 x 256 tiles and 0.92 with 128 x 128; the gradient's products of 301 x
-// 8009 x 520 in f32 36 + 34 + 40 us with 64 x 64 and 48 + 50 + 52 with 128 x 128;
-// losses of 48 x 128003 x 4096 in bf16 188 us with the narrow tile and 201 with
-// 64 x 64 (of 48 x 32000 x 2048 in f32, bound by the f32 instructions, 92 and 85).
+// f32 takes 64 x 64 tiles throughout: its matrix instructions, an eighth as
+// fast as the 16-bit ones, are the bound, so what counts is how little a ragged
+// edge wastes and how evenly the CUs are filled.  Gradients of 563 x 79903 x 620
+// take 1.4 ms so and 2.7 with the larger ones, of 2048 x 32000 x 2048 6.2 and 6.3,
+// losses of 48 x 32000 x 2048 85 us and 92 with the narrow one.
+// 16-bit types: 256 x 256 tiles where they fill four fifths of the CUs, 128 x
+// 128 where they reach two per CU (they run two to a CU), 64 x 64 below; for up
+// to 64 tokens the tile that is 64 wide.  Losses of 4096 x 50257 x 2048 in f16
+// take 0.75 ms with 256 x 256 tiles and 0.92 with 128 x 128; losses of 411 x
+// 81749 x 3056 in bf16 0.32 ms with 128 x 128 and 0.50 with 64 x 64; losses of 48
+// x 128003 x 4096 in bf16 188 us with the narrow tile and 201 with 64 x 64.
 enum Shape { kBig, kMid, kThin, kSmall };
 template <class F>
-Shape shape_of(uint32_t tokens, int cus, F tiles) {
+Shape shape_of(DType type, uint32_t tokens, int cus, F tiles) {
+  if (type == DType::F32) return kSmall;
   if (tokens > 128 && tiles(256u) * 5 >= (uint64_t)cus * 4) return kBig;
   if (tokens <= 64) return kThin;
   return tiles(128u) >= 2 * (uint64_t)cus ? kMid : kSmall;
@@ -435,16 +440,19 @@ constexpr uint32_t kBmOf[] = {256, 128, 128, 64};
 // Calls f with the tile type of a shape.
 template <DType T, OperandKind A, OperandKind B, class F>
 hipError_t with_tile(Shape s, F f) {
-  switch (s) {
-    case kBig: return f(Big<T, A, B>());
-    case kMid: return f(Mid<T, A, B>());
-    case kThin: return f(Thin<T, A, B>());
-    default: return f(Small<T, A, B>());
+  if constexpr (T != DType::F32) {
+    switch (s) {
+      case kBig: return f(Big<T, A, B>());
+      case kMid: return f(Mid<T, A, B>());
+      case kThin: return f(Thin<T, A, B>());
+      default: break;
+    }
   }
+  return f(Small<T, A, B>());
 }
 
 Shape logits_shape(const XentArgs& a, const Shards& s) {
-  return shape_of(a.tokens, a.cus, [&](uint32_t b) { return (uint64_t)tiles_of(s, b) * ceil_div(a.tokens, b); });
+  return shape_of(a.type, a.tokens, a.cus, [&](uint32_t b) { return (uint64_t)tiles_of(s, b) * ceil_div(a.tokens, b); });
 }
 
 template <DType T, class K>
@@ -526,7 +534,7 @@ hipError_t launch_dw(const Shards& run, DwTile p, hipStream_t s) {
 }
 
 Shape dx_shape(const XentArgs& a, uint32_t splits) {
-  return shape_of(a.tokens, a.cus,
+  return shape_of(a.type, a.tokens, a.cus,
                   [&](uint32_t b) { return (uint64_t)ceil_div(a.dim, b) * ceil_div(a.tokens, b) * splits; });
 }
 
@@ -589,7 +597,7 @@ hipError_t grad_of(const XentArgs& a, const Shards& all, char* ws, hipStream_t s
       p.dim = a.dim;
       p.vpitch = m.vpitch;
       // its second operand is the vocabulary: never the narrow tile
-      const Shape shape = shape_of(a.tokens <= 64 ? 128 : a.tokens, a.cus,
+      const Shape shape = shape_of(a.type, a.tokens <= 64 ? 128 : a.tokens, a.cus,
                                    [&](uint32_t b) { return (uint64_t)ceil_div(a.dim, b) * tiles_of(run, b); });
       e = with_tile<T, kCols, kCols>(shape, [&](auto k) { return launch_dw<T, decltype(k)>(run, p, s); });
       if (e) return e;
@@ -621,7 +629,7 @@ XentLossSpace xent_loss_space(const XentArgs& a, const Shards& all) {
 // four fifths of the CUs; otherwise until its 128 x 128 tiles reach two per CU,
 // at most 64 ways.  Gradients of 4096 x 50000 x 2048 in bf16 take 2.20 ms in
 // two shares of large tiles, 2.42 in two of small ones; 2500 x 8000 x 2048 (240
-// tiles) 0.27 and 0.29; 2048 x 32000 x 2048 in f32 6.46 and 6.34.
+// tiles) 0.27 and 0.29.
 XentGradSpace xent_grad_space(const XentArgs& a, const Shards& all, bool dx, bool dw) {
   XentGradSpace m;
   const size_t es = (size_t)elem_size(a.type);
