@@ -2,6 +2,8 @@
 //   p_t = softmax(z_t),  f_e = count_e / (N k),  P_e = (1/N) sum_t p_te,
 //   L = coef E sum_e f_e P_e,
 //   dL/dz_te = coef (E/N) p_te (f_e - sum_e' f_e' p_te'),
+// where any constant may be taken from f, as sum_e p_te = 1; the kernels take
+// 1/E, so that shares that are nearly equal do not cancel in 32 bits,
 // N the counted tokens of all ranks (those with at least one chosen expert).
 //
 // Three launches.  balance_rows reads every logit once: a group of lanes
@@ -167,6 +169,7 @@ __device__ __forceinline__ uint32_t rank_of(const BalanceGrid& g, uint32_t nrank
 }
 
 constexpr int kJoinExperts = 16, kJoinLanes = 64, kJoinThreads = kJoinExperts * kJoinLanes;
+static_assert(kJoinLanes == kMaxRanks, "a lane per rank clears and writes its counts");
 
 // What the launches leave to each other.
 struct BalanceSums {
@@ -174,7 +177,7 @@ struct BalanceSums {
   uint32_t* pcount;        // [workgroup][expert] choices
   uint32_t* pvalid;        // [workgroup] rows that take part
   double* term;            // [expert] f P
-  float* f;                // [expert]
+  float* f;                // [expert] f - 1/E
   float* scale;            // coef E / N
 };
 
@@ -285,7 +288,7 @@ __global__ __launch_bounds__(kJoinThreads) void balance_join(BalanceArgs a, Bala
     for (int i = 0; i < kJoinLanes; ++i) s += dsum[i][le];
     a.counts[(uint64_t)a.nranks * a.nexperts + e] = (int64_t)c;
     const double share = nvalid ? (double)c / ((double)nvalid * a.topk) : 0.0;
-    p.f[e] = (float)share;
+    p.f[e] = (float)(share - 1.0 / a.nexperts);
     p.term[e] = nvalid ? share * (s / (double)nvalid) : 0.0;
     if (e == 0) *p.scale = nvalid ? (float)((double)a.coef * a.nexperts / (double)nvalid) : 0.0f;
   }
