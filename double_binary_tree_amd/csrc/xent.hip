@@ -20,7 +20,10 @@
 // q_ty, near -1 and then nearly exact, and with equal weights, as in a mean, x'
 // is x.  With dloss_t in the stored g the rounding of that one entry was common
 // to a whole row of both gradients: for a dozen tokens dw in bf16 was off by
-// 3.3e-3 in norm, where rounding the result alone gives 1.7e-3.
+// 3.3e-3 in norm, where rounding the result alone gives 1.7e-3.  Up to 64
+// tokens, where roundings do not average out and the products are bound by the
+// vocabulary's rows, g / D is stored as hi + lo, two rows per token: dx is the
+// sum of two rows' products, dw sums over twice the tokens, of x as it is.
 //
 // Vocabulary rows are the product's first operand (lanes hold 4 consecutive
 // rows of one token), so a token's maximum and sum are mostly within a lane.
@@ -170,6 +173,10 @@ __global__ __launch_bounds__(kJoinTokens* kJoinLanes) void xent_join(
 template <DType T>
 constexpr float kStored = T == DType::F16 ? 16384.0f : 1.0f;
 
+// Whether g / D is stored as hi + lo: row t of the hi parts, row tokens + t of
+// the lo parts.
+__host__ __device__ constexpr bool two_rows(DType type, uint32_t tokens) { return type != DType::F32 && tokens <= 64; }
+
 // weight[0] = D, the largest |dloss| of the tokens with a loss, weight[1] = D
 // over what q was multiplied by.
 __global__ __launch_bounds__(1024) void xent_weight(const float* __restrict__ dloss, const int64_t* __restrict__ targets,
@@ -192,11 +199,12 @@ __global__ __launch_bounds__(1024) void xent_weight(const float* __restrict__ dl
 }
 
 // x (16-bit types: x') with zeros in the rows of tokens without a loss: such a
-// token then adds nothing to dw, whatever its hidden state holds.
+// token then adds nothing to dw, whatever its hidden state holds.  With two rows
+// per token x comes twice.
 template <DType T>
 __global__ __launch_bounds__(256) void xent_clean(const u32x4* __restrict__ x, const int64_t* __restrict__ targets,
                                                   const float* __restrict__ dloss, const float* __restrict__ weight,
-                                                  uint64_t vecs, uint32_t per_token, int64_t vocab,
+                                                  uint64_t vecs, uint32_t per_token, int64_t vocab, bool two,
                                                   u32x4* __restrict__ out) {
   typedef typename Elem<T>::type E;
   typedef E EV __attribute__((ext_vector_type(16 / sizeof(E))));
@@ -207,7 +215,7 @@ __global__ __launch_bounds__(256) void xent_clean(const u32x4* __restrict__ x, c
     if (y >= 0 && y < vocab) {
       v = x[i];
       if constexpr (sizeof(E) == 2) {
-        const float big = weight[0], f = big > 0.0f ? dloss[t] / big : 0.0f;
+        const float big = weight[0], f = two ? 1.0f : big > 0.0f ? dloss[t] / big : 0.0f;
         EV e = bits<EV>(v);
 #pragma unroll
         for (int k = 0; k < 8; ++k) e[k] = (E)((float)e[k] * f);
@@ -215,6 +223,7 @@ __global__ __launch_bounds__(256) void xent_clean(const u32x4* __restrict__ x, c
       }
     }
     out[i] = v;
+    if (two) out[vecs + i] = v;
   }
 }
 
@@ -223,12 +232,13 @@ struct GradTile {
   const int64_t* targets;
   const float* lse;
   const float* dloss;
+  const float* weight;         // with two rows per token
   void* g;
   uint32_t tokens, dim, vpitch, tm, tn, band;
   int64_t vocab;
 };
 
-// g (16-bit types: q) of the run's rows for every token.  Positions between a rank's last row
+// g (16-bit types: q, or g / D in two rows) of the run's rows for every token.  Positions between a rank's last row
 // and the next multiple of kShardAlign become zeros: the products that read g
 // go over whole vectors.
 template <DType T, class K>
@@ -253,6 +263,8 @@ __global__ __launch_bounds__(K::threads) void xent_dlogits(Shards sh, GradTile p
   E* g = static_cast<E*>(p.g);
   const RowStage<K, K::WM * 2, K::WN> stage(lds_address(lds), wave, lane);
   if constexpr (ES == 2) __syncthreads();
+  const bool two = ES == 2 && K::BN == 64 && p.weight;     // up to 64 tokens take the narrow tile
+  const float over = two && p.weight[0] > 0.0f ? kStored<T> / p.weight[0] : 0.0f;
 #pragma unroll
   for (int j = 0; j < K::NF; ++j) {
     const uint32_t t = tok + wn * K::WN + j * 16 + (lane & 15), tt = min(t, p.tokens - 1);
@@ -260,7 +272,7 @@ __global__ __launch_bounds__(K::threads) void xent_dlogits(Shards sh, GradTile p
     const bool counted = id >= 0 && id < p.vocab;
     const int64_t at = id - (int64_t)sh.id0[r] - row;
     const int y = at >= 0 && at < rows ? (int)at : -1;
-    const float lse = p.lse[tt], d = ES == 2 ? kStored<T> : p.dloss[tt];
+    const float lse = p.lse[tt], d = two ? p.dloss[tt] * over : ES == 2 ? kStored<T> : p.dloss[tt];
 #pragma unroll
     for (int i = 0; i < K::MF; ++i) {
       const int v = wm * K::WM + i * 16 + 4 * (lane >> 4);
@@ -268,15 +280,32 @@ __global__ __launch_bounds__(K::threads) void xent_dlogits(Shards sh, GradTile p
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
         const float q = exp_of(acc[i][j][e] - lse) - (v + e == y ? 1.0f : 0.0f);
-        out[e] = (E)(counted && v + e < rows ? d * q : 0.0f);
+        const float x = counted && v + e < rows ? d * q : 0.0f;
+        out[e] = (E)x;
+        acc[i][j][e] = x - (float)out[e];                  // lo
       }
       if constexpr (ES == 2) stage.put(j * 16 + (lane & 15), (i * 16 + 4 * (lane >> 4)) * 2, out);
       else if (v < padded && t < p.tokens) *reinterpret_cast<E4*>(g + (uint64_t)t * p.vpitch + first + v) = out;
     }
   }
-  if constexpr (ES == 2)
-    stage.store(reinterpret_cast<char*>(g + (uint64_t)(tok + wn * K::WN) * p.vpitch + first + wm * K::WM), (uint64_t)p.vpitch * ES,
-                (int)(p.tokens - tok) - wn * K::WN, (padded - wm * K::WM) * ES);
+  if constexpr (ES == 2) {
+    const int left = (int)(p.tokens - tok) - wn * K::WN, bytes = (padded - wm * K::WM) * ES;
+    char* to = reinterpret_cast<char*>(g + (uint64_t)(tok + wn * K::WN) * p.vpitch + first + wm * K::WM);
+    const uint64_t pitch = (uint64_t)p.vpitch * ES;
+    stage.store(to, pitch, left, bytes);
+    if (two) {
+#pragma unroll
+      for (int j = 0; j < K::NF; ++j)
+#pragma unroll
+        for (int i = 0; i < K::MF; ++i) {
+          E4 out;
+#pragma unroll
+          for (int e = 0; e < 4; ++e) out[e] = (E)acc[i][j][e];
+          stage.put(j * 16 + (lane & 15), (i * 16 + 4 * (lane >> 4)) * 2, out);
+        }
+      stage.store(to + p.tokens * pitch, pitch, left, bytes);
+    }
+  }
 }
 
 // dx: first operand the run's rows as they lie in memory (columns of k), second
@@ -329,13 +358,14 @@ __global__ __launch_bounds__(K::threads) void xent_dx(Shards sh, DxTile p) {
   }
 }
 
-// dx = the sum of the parts, in order (16-bit types: times dloss), rounded once;
-// zeros for a token without a loss.  Four values a lane (dim is a multiple of 4).
+// dx = the sum of the parts, in order (16-bit types: times dloss, or with two
+// rows per token, whose second is a part of its own, times D), rounded once; zeros
+// for a token without a loss.  Four values a lane (dim is a multiple of 4).
 template <DType T>
 __global__ __launch_bounds__(256) void xent_dx_join(const float* __restrict__ part, uint32_t splits, uint64_t quads,
                                                     uint32_t per_token, const int64_t* __restrict__ targets,
                                                     int64_t vocab, const float* __restrict__ dloss,
-                                                    void* __restrict__ dx) {
+                                                    const float* __restrict__ weight, void* __restrict__ dx) {
   typedef typename Elem<T>::type E;
   typedef E E4 __attribute__((ext_vector_type(4)));
   for (uint64_t q = (uint64_t)blockIdx.x * 256 + threadIdx.x; q < quads; q += (uint64_t)gridDim.x * 256) {
@@ -344,7 +374,7 @@ __global__ __launch_bounds__(256) void xent_dx_join(const float* __restrict__ pa
     const uint64_t t = q / per_token;
     const int64_t y = targets[t];
     const bool counted = y >= 0 && y < vocab;
-    const float f = sizeof(E) == 2 ? dloss[t] / kStored<T> : 1.0f;
+    const float f = sizeof(E) == 4 ? 1.0f : weight ? weight[1] : dloss[t] / kStored<T>;
     E4 out;
 #pragma unroll
     for (int e = 0; e < 4; ++e) out[e] = (E)(counted ? s[e] * f : 0.0f);
@@ -533,9 +563,9 @@ hipError_t launch_dw(const Shards& run, DwTile p, hipStream_t s) {
   return hipGetLastError();
 }
 
-Shape dx_shape(const XentArgs& a, uint32_t splits) {
-  return shape_of(a.type, a.tokens, a.cus,
-                  [&](uint32_t b) { return (uint64_t)ceil_div(a.dim, b) * ceil_div(a.tokens, b) * splits; });
+Shape dx_shape(const XentArgs& a, uint32_t rows, uint32_t splits) {
+  return shape_of(a.type, rows, a.cus,
+                  [&](uint32_t b) { return (uint64_t)ceil_div(a.dim, b) * ceil_div(rows, b) * splits; });
 }
 
 template <DType T>
@@ -546,22 +576,25 @@ hipError_t grad_of(const XentArgs& a, const Shards& all, char* ws, hipStream_t s
   for (uint32_t r = 0; r < all.nranks; ++r) dw = dw || all.dw[r] != nullptr;
   const XentGradSpace m = xent_grad_space(a, all, dx, dw);
   float* weight = reinterpret_cast<float*>(ws + m.weight);
+  const bool two = two_rows(T, a.tokens);
+  const uint32_t rows = two ? 2 * a.tokens : a.tokens;
   int64_t vocab = 0;
   for (uint32_t r = 0; r < all.nranks; ++r) vocab += all.rows[r];
   hipError_t e;
+  if (two || (ES == 2 && dw))
+    hipLaunchKernelGGL(xent_weight, dim3(1), dim3(1024), 0, s, a.dloss, a.targets, a.tokens, vocab, kStored<T>, weight);
   if (dw) {
-    if (ES == 2)
-      hipLaunchKernelGGL(xent_weight, dim3(1), dim3(1024), 0, s, a.dloss, a.targets, a.tokens, vocab, kStored<T>, weight);
     const uint64_t vecs = (uint64_t)a.tokens * a.dim * ES / kVecBytes;
     hipLaunchKernelGGL(xent_clean<T>, dim3((uint32_t)std::min<uint64_t>((vecs + 255) / 256, (uint64_t)a.cus * 16)), dim3(256),
                        0, s, static_cast<const u32x4*>(a.x), a.targets, a.dloss, weight, vecs,
-                       (uint32_t)(a.dim * ES / kVecBytes), vocab, reinterpret_cast<u32x4*>(ws + m.x));
+                       (uint32_t)(a.dim * ES / kVecBytes), vocab, two, reinterpret_cast<u32x4*>(ws + m.x));
   }
   GradTile gp{};
   gp.x = a.x;
   gp.targets = a.targets;
   gp.lse = a.lse;
   gp.dloss = a.dloss;
+  gp.weight = two ? weight : nullptr;
   gp.g = ws + m.g;
   gp.tokens = a.tokens;
   gp.dim = a.dim;
@@ -578,13 +611,13 @@ hipError_t grad_of(const XentArgs& a, const Shards& all, char* ws, hipStream_t s
       DxTile p{};
       p.g = ws + m.g;
       p.part = reinterpret_cast<float*>(ws + m.part);
-      p.tokens = a.tokens;
+      p.tokens = rows;
       p.dim = a.dim;
       p.vpitch = m.vpitch;
       p.share = (uint32_t)align_up(ceil_div(run.width, m.splits), 64);
       p.add = add;
       add = true;
-      e = with_tile<T, kCols, kRows>(dx_shape(a, m.splits),
+      e = with_tile<T, kCols, kRows>(dx_shape(a, rows, m.splits),
                                      [&](auto k) { return launch_dx<T, decltype(k)>(run, p, m.splits, s); });
       if (e) return e;
     }
@@ -593,7 +626,7 @@ hipError_t grad_of(const XentArgs& a, const Shards& all, char* ws, hipStream_t s
       p.x = ws + m.x;
       p.g = ws + m.g;
       p.weight = weight;
-      p.tokens = a.tokens;
+      p.tokens = rows;
       p.dim = a.dim;
       p.vpitch = m.vpitch;
       // its second operand is the vocabulary: never the narrow tile
@@ -606,8 +639,8 @@ hipError_t grad_of(const XentArgs& a, const Shards& all, char* ws, hipStream_t s
   if (dx) {
     const uint64_t quads = (uint64_t)a.tokens * a.dim / 4;
     hipLaunchKernelGGL(xent_dx_join<T>, dim3((uint32_t)std::min<uint64_t>((quads + 255) / 256, (uint64_t)a.cus * 16)),
-                       dim3(256), 0, s, reinterpret_cast<const float*>(ws + m.part), m.splits, quads,
-                       a.dim / 4, a.targets, vocab, a.dloss, a.dx);
+                       dim3(256), 0, s, reinterpret_cast<const float*>(ws + m.part), two ? 2 * m.splits : m.splits, quads,
+                       a.dim / 4, a.targets, vocab, a.dloss, two ? weight : nullptr, a.dx);
   }
   return hipGetLastError();
 }
@@ -633,12 +666,13 @@ XentLossSpace xent_loss_space(const XentArgs& a, const Shards& all) {
 XentGradSpace xent_grad_space(const XentArgs& a, const Shards& all, bool dx, bool dw) {
   XentGradSpace m;
   const size_t es = (size_t)elem_size(a.type);
+  const uint32_t rows = two_rows(a.type, a.tokens) ? 2 * a.tokens : a.tokens;
   uint64_t positions = 0;
   for (uint32_t r = 0; r < all.nranks; ++r) positions += align_up(all.rows[r], kShardAlign);
   m.width = (uint32_t)std::min<uint64_t>(positions, std::max<uint64_t>(4096, (((uint64_t)1 << 28) / a.tokens) / 256 * 256));
   m.vpitch = (uint32_t)align_up(m.width, 64);
-  const uint64_t tiles = (uint64_t)ceil_div(a.dim, 128) * ceil_div(a.tokens, 128), cus = a.cus;
-  const uint64_t big = (uint64_t)ceil_div(a.dim, 256) * ceil_div(a.tokens, 256);
+  const uint64_t tiles = (uint64_t)ceil_div(a.dim, 128) * ceil_div(rows, 128), cus = a.cus;
+  const uint64_t big = (uint64_t)ceil_div(a.dim, 256) * ceil_div(rows, 256);
   const uint64_t shares = std::min<uint64_t>(4, std::max<uint64_t>(1, cus / big));
   if (es == 2 && a.tokens > 128 && m.width / shares >= 256 && big * shares * 5 >= cus * 4) m.splits = (uint32_t)shares;
   else
@@ -646,9 +680,9 @@ XentGradSpace xent_grad_space(const XentArgs& a, const Shards& all, bool dx, boo
   size_t at = 0;
   auto take = [&](size_t n) { const size_t p = at; at = align_up(at + n, 256); return p; };
   m.weight = take(2 * sizeof(float));
-  m.g = take((size_t)a.tokens * m.vpitch * es);
-  if (dw) m.x = take((size_t)a.tokens * a.dim * es);
-  if (dx) m.part = take((size_t)m.splits * a.tokens * a.dim * sizeof(float));
+  m.g = take((size_t)rows * m.vpitch * es);
+  if (dw) m.x = take((size_t)rows * a.dim * es);
+  if (dx) m.part = take((size_t)m.splits * rows * a.dim * sizeof(float));
   m.bytes = at;
   return m;
 }

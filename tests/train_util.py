@@ -73,16 +73,22 @@ def xent_bounds(x, ws, targets, lse, dloss, dtype):
     dg = np.abs(dloss)[:, None] * q * (dz + (np.abs(z - lse[:, None]) + 4) * 4 * U32) + np.abs(g) * 4 * U32
     dg[~ok] = 0.0
     # stored in the buffer type: f32 as it is, 16-bit types as q = g / dloss
-    # (f16: times 2^14, so that its smallest step is 2^-24 / 2^14 of |dloss|)
+    # (f16: times 2^14, so that its smallest step is 2^-24 / 2^14 of |dloss|); up
+    # to 64 tokens g / top as hi + lo: half a step of lo, which is half a step of
+    # hi or less
     top = np.abs(dloss[ok]).max() if ok.any() else 0.0
-    dg += np.abs(g) * ROUND[dtype] + (top * 2.0 ** -38 if dtype == "f16" else TINY[dtype] * max(1.0, top))
+    two = dtype != "f32" and len(x) <= 64
+    stored = ROUND[dtype] ** 2 + 4 * U32 if two else ROUND[dtype]
+    dg += np.abs(g) * stored + (top * 2.0 ** -38 if dtype == "f16" else TINY[dtype] * max(1.0, top))
     dg[~ok] = 0.0
     xs = np.where(ok[:, None], np.abs(x), 0.0)
     size_dx, size_dw = np.abs(g) @ np.abs(w), np.abs(g).T @ xs
-    # a 16-bit dx is multiplied by dloss (one rounding in f32)
-    dx_tol = dg @ np.abs(w) + (sum_bound(len(w)) + U32) * size_dx
-    dw_tol = dg.T @ xs + sum_bound(len(x)) * size_dw
-    if dtype != "f32":
+    # a 16-bit dx is multiplied by dloss (one rounding in f32); hi and lo are
+    # summed apart, their magnitudes at most 1 + ROUND of the whole
+    twice = 1 + 2 * ROUND[dtype] if two else 1.0
+    dx_tol = dg @ np.abs(w) + (twice * sum_bound(len(w)) + 3 * U32) * size_dx
+    dw_tol = dg.T @ xs + twice * sum_bound(2 * len(x)) * size_dw
+    if dtype != "f32" and not two:
         # x' = x dloss / top: two roundings in f32, one to the type (half of its
         # smallest step where that is more); dw is multiplied by top (over 2^14)
         dw_tol += (ROUND[dtype] + 4 * U32) * size_dw + TINY[dtype] / 2 * top * q[ok].sum(0)[:, None] + TINY[dtype] * top * len(x)
