@@ -6,7 +6,6 @@
 
 #include <algorithm>
 #include <cmath>
-#include <vector>
 
 namespace emu {
 namespace {
@@ -28,13 +27,18 @@ int current_cus() {
 // The buffers of a call: an output overlaps nothing else.
 struct Spans {
   struct Span { uintptr_t lo, hi; bool out; };
-  std::vector<Span> all;
-  void in(const void* p, uint64_t bytes) { if (bytes) all.push_back({(uintptr_t)p, (uintptr_t)p + bytes, false}); }
-  void out(const void* p, uint64_t bytes) { if (bytes) all.push_back({(uintptr_t)p, (uintptr_t)p + bytes, true}); }
+  Span all[3 * kMaxRanks + 6];           // three per rank, and a call's own
+  int count = 0;
+  void add(const void* p, uint64_t bytes, bool out) {
+    if (bytes) all[count++] = {(uintptr_t)p, (uintptr_t)p + bytes, out};
+  }
+  void in(const void* p, uint64_t bytes) { add(p, bytes, false); }
+  void out(const void* p, uint64_t bytes) { add(p, bytes, true); }
   bool clash() {
-    std::sort(all.begin(), all.end(), [](const Span& x, const Span& y) { return x.lo < y.lo; });
+    std::sort(all, all + count, [](const Span& x, const Span& y) { return x.lo < y.lo; });
     uintptr_t in_end = 0, out_end = 0;
-    for (const Span& s : all) {
+    for (const Span* at = all; at < all + count; ++at) {
+      const Span& s = *at;
       if (s.lo < out_end || (s.out && s.lo < in_end)) return true;
       uintptr_t& end = s.out ? out_end : in_end;
       end = std::max(end, s.hi);
@@ -44,7 +48,8 @@ struct Spans {
 };
 
 constexpr uint64_t kMaxTokens = (uint64_t)1 << 20, kMaxDim = (uint64_t)1 << 16, kMaxVocab = (uint64_t)1 << 24;
-constexpr uint64_t kMaxLogits = (uint64_t)1 << 37, kMaxRouterTokens = (uint64_t)1 << 24;
+// at 64 x 64 logits a workgroup, 2^35 keep a grid below 2^32 threads
+constexpr uint64_t kMaxLogits = (uint64_t)1 << 35, kMaxRouterTokens = (uint64_t)1 << 24;
 
 // The checks that size the workspace, and the shards they describe.
 int xent_sizes(int nranks, const size_t vocab[], size_t tokens, size_t dim, int dtype, XentArgs* a, Shards* all) {

@@ -264,7 +264,7 @@ __global__ __launch_bounds__(K::threads) void xent_dlogits(Shards sh, GradTile p
   const RowStage<K, K::WM * 2, K::WN> stage(lds_address(lds), wave, lane);
   if constexpr (ES == 2) __syncthreads();
   const bool two = ES == 2 && K::BN == 64 && p.weight;     // up to 64 tokens take the narrow tile
-  const float over = two && p.weight[0] > 0.0f ? kStored<T> / p.weight[0] : 0.0f;
+  const float big = two ? p.weight[0] : 0.0f;
 #pragma unroll
   for (int j = 0; j < K::NF; ++j) {
     const uint32_t t = tok + wn * K::WN + j * 16 + (lane & 15), tt = min(t, p.tokens - 1);
@@ -272,7 +272,7 @@ __global__ __launch_bounds__(K::threads) void xent_dlogits(Shards sh, GradTile p
     const bool counted = id >= 0 && id < p.vocab;
     const int64_t at = id - (int64_t)sh.id0[r] - row;
     const int y = at >= 0 && at < rows ? (int)at : -1;
-    const float lse = p.lse[tt], d = two ? p.dloss[tt] * over : ES == 2 ? kStored<T> : p.dloss[tt];
+    const float lse = p.lse[tt], d = two ? (big > 0.0f ? p.dloss[tt] / big * kStored<T> : 0.0f) : ES == 2 ? kStored<T> : p.dloss[tt];
 #pragma unroll
     for (int i = 0; i < K::MF; ++i) {
       const int v = wm * K::WM + i * 16 + 4 * (lane >> 4);

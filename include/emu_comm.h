@@ -454,15 +454,16 @@ int emu_stream_probe(int kind, const void* src, void* dst, size_t bytes, void* s
  *   vocab    any sizes, 0 allowed (w[r] is then not read); at least one row
  *            in all; tokens == 0 is a successful no-op (its dw: zeros)
  * Products are summed in f32.  Limits: tokens <= 2^20, dim <= 2^16,
- * vocabulary <= 2^24 rows, tokens * vocabulary <= 2^37.
+ * vocabulary <= 2^24 rows, tokens * vocabulary <= 2^35.
  *
  * emu_cross_entropy_grad - the gradients, for dloss[t] = d L / d loss[t]
  * (f32) and the lse of a forward call:
  *   g_tv = dloss[t] (exp(z_tv - lse[t]) - [v = targets[t]]), 0 without a loss
  *   dx = g w (over all ranks),  dw[r] = g_r^T x
- * in dtype, rounded once from f32 sums; g itself is rounded to dtype before
- * these products (f16: after scaling by a power of two that follows the
- * largest |dloss|).  A token without a loss adds nothing to dw, whatever its
+ * in dtype, rounded once from f32 sums.  16-bit types round exp(z - lse) - [..]
+ * to dtype before these products, and for dw the rows of x times dloss over its
+ * largest magnitude; up to 64 tokens g keeps twice dtype's bits instead.  f32
+ * rounds g.  A token without a loss adds nothing to dw, whatever its
  * hidden state holds, and its row of dx is 0.  dx or dw may be NULL (not
  * wanted; not both); dw[r] of a rank with rows must not be NULL if dw is
  * given.

@@ -145,6 +145,29 @@ def test_cross_entropy_gradient_against_differences_of_its_own_loss(dtype):
     assert (np.abs(U.exact(up) - U.exact(down) - slope) <= tol).all()
 
 
+@pytest.mark.parametrize("dtype", ["f32", "f16", "bf16"])
+@pytest.mark.parametrize("tokens", [5, 70])
+def test_cross_entropy_gradient_of_tiny_and_zero_weights(tokens, dtype):
+    from double_binary_tree_amd import emucomm as E
+    announce(f"cross entropy gradients of tiny and zero weights, {tokens} tokens {dtype}")
+    x, ws, y, yt = xent_case([40, 23], tokens, 24, dtype)
+    _, lse = run_loss(E, x, ws, yt)
+    big = max(float(x.abs().max()), max(float(w.abs().max()) for w in ws))
+    for weight in (0.0, 1e-39, 1e-45):       # 1e-39 and 1e-45 have no normal f32
+        d = torch.full((tokens,), weight, device="cuda")
+        d[0] = weight / 3
+        dx, dws = run_grad(E, x, ws, yt, lse, d)
+        for t in [dx, *dws]:                 # |g| is at most dloss and sums to at most 2 dloss over a row
+            assert float(t.abs().max()) <= 2 * weight * big * tokens * 1.01
+    # one weight far above the others
+    d = torch.full((tokens,), 1e-30, device="cuda")
+    d[1] = 1e6 if dtype != "f16" else 100.0
+    dx, dws = run_grad(E, x, ws, yt, lse, d)
+    want_dx, want_dw = O.cross_entropy_grad(U.exact(x), [U.exact(w) for w in ws], y, U.exact(lse), U.exact(d))
+    for got, want in [(dx, want_dx), *zip(dws, want_dw)]:
+        assert np.linalg.norm(U.exact(got) - want) <= 2 * U.ROUND[dtype] * np.linalg.norm(want) + 1e-5 * np.linalg.norm(want)
+
+
 def test_cross_entropy_masked_tokens_do_not_leak():
     from double_binary_tree_amd import emucomm as E
     announce("cross entropy: NaN and infinities in tokens without a loss")

@@ -24,7 +24,7 @@ def grad(vocab=(10, 6), tokens=4, dim=16, dtype=F32, x=P[0], w=(P[1], P[2]), y=P
 @pytest.mark.parametrize("change", [
     {"dtype": I32}, {"dtype": 9}, {"vocab": ()}, {"vocab": (0, 0)}, {"dim": 0}, {"dim": 17}, {"dim": 18}, {"dim": 1 << 17},
     {"dim": 12, "dtype": F16}, {"dim": 12, "dtype": BF16}, {"tokens": (1 << 20) + 1}, {"vocab": ((1 << 24) + 1, 6)},
-    {"vocab": (1 << 23, (1 << 23) + 1)}, {"vocab": (1 << 18, 0), "tokens": (1 << 20)}, {"x": None}, {"x": A + 4}, {"w": None},
+    {"vocab": (1 << 23, (1 << 23) + 1)}, {"vocab": (1 << 18, 0), "tokens": (1 << 20)}, {"vocab": (1 << 15, 1), "tokens": (1 << 20)}, {"x": None}, {"x": A + 4}, {"w": None},
     {"w": (P[1], None)}, {"w": (P[1] + 8, P[2])}, {"y": None}, {"y": P[3] + 8}, {"lse": None}, {"ws": None},
     {"ws": P[6] + 8}, {"size": 0}, {"ws": P[1]}, {"vocab": (1,) * 65, "w": (P[1],) * 65}])
 def test_cross_entropy_refuses(change):
