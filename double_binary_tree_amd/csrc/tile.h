@@ -447,7 +447,9 @@ __device__ __forceinline__ uint32_t xcd_share(uint32_t w, uint32_t total) {
 }
 
 // Item t of tm x tn tiles, walked in bands of `band` tile rows: the tiles that
-// one XCD works on at a time share rows of both operands.
+// one XCD works on at a time share rows of both operands.  (Gradients of 8192 x
+// 100277 x 4096 in bf16: bands of 4 and 8 17.0 ms, of 16 17.9; losses of 4096 x
+// 50257 x 2048 in f16: 765, 753 and 758 us.)
 __device__ __forceinline__ void tile_of(uint32_t t, uint32_t tm, uint32_t tn, uint32_t band, uint32_t& m, uint32_t& n) {
   const uint32_t per = band * tn, g = t / per, first = g * band, rows = min(band, tm - first);
   t -= g * per;

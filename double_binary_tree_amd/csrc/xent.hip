@@ -70,6 +70,9 @@ __device__ __forceinline__ void merge(float& m, float& s, float m2, float s2) {
   m = big;
 }
 
+// Bound by the matrix instructions with many tokens (4096 x 50257 x 2048 in f16
+// 0.75 ms, 1.12 PFLOP/s; the exponentials of a tile, about a tenth, are not
+// overlapped), by reading w with few (48 x 128003 x 4096 in bf16 183 us, 5.7 TB/s).
 struct LossTile {
   const void* x;
   const int64_t* targets;
@@ -238,6 +241,8 @@ struct GradTile {
   int64_t vocab;
 };
 
+// Bound by the matrix instructions: a run of 8192 x 32768 x 4096 in bf16 takes
+// 1.82 ms, 1.21 PFLOP/s, 0.1 ms of it writing g.
 // g (16-bit types: q, or g / D in two rows) of the run's rows for every token.  Positions between a rank's last row
 // and the next multiple of kShardAlign become zeros: the products that read g
 // go over whole vectors.
@@ -310,7 +315,8 @@ __global__ __launch_bounds__(K::threads) void xent_dlogits(Shards sh, GradTile p
 
 // dx: first operand the run's rows as they lie in memory (columns of k), second
 // g [tokens][vpitch]; the sum over the run goes rank by rank, and workgroup y
-// of gridDim.y sums a share of its positions into part[y].
+// of gridDim.y sums a share of its positions into part[y].  1.81 ms for the same
+// run, 1.21 PFLOP/s.
 struct DxTile {
   const void* g;
   float* part;
@@ -390,7 +396,8 @@ __global__ __launch_bounds__(256) void xent_zero(Shards sh, uint64_t row_bytes) 
 }
 
 // dw: both operands as columns of k (tokens): x [tokens][dim] and g [tokens]
-// [vpitch].
+// [vpitch].  2.04 ms for the same run, 1.08 PFLOP/s: both operands go through
+// the transpose read, twice the LDS instructions of rows.
 struct DwTile {
   const void* x;
   const void* g;
