@@ -531,14 +531,23 @@ uint32_t triangle_tiles(uint32_t m, uint32_t b) {
 // 3.40 unsplit; 4 x 1024 x 8192 in f32 (six) 1.84 and 1.87; 1 x 2048 x 8192 in
 // f32 (seven) 1.76 and 1.72; 4 x 1024 x 4096 in f32 (six, shorter k) 1.10 and
 // 0.94; 2 x 2048 x 16384 in bf16 (three) 2.77 and 3.01.
+// Where even 64 x 64 tiles leave CUs idle, k is split into shares of 512 until
+// there are two workgroups per CU, in up to sixteen: 2 x 17 x 7412 in f32 130 us,
+// 543 unsplit; 8 x 128 x 1024 in f32 (two) 131 and 141, in bf16 (two, therefore
+// not taken) 101 and 97; 1 x 512 x 2048 in bf16 (four) 144 and 183.
 constexpr uint32_t kSplitWork = 16384;   // k times products
 Choice choose_sym(const OrthoMat& q, int cus, uint32_t nmat, uint32_t k, bool pairs) {
   const Choice c = choose(cus, nmat, [&](uint32_t b) { return triangle_tiles(q.m, b); });
   const uint64_t big = (uint64_t)triangle_tiles(q.m, 256) * nmat;
-  if (c.shape == kBig || (uint64_t)k * (pairs ? 3 : 1) < kSplitWork) return c;
+  if (c.shape == kBig) return c;
   const uint32_t splits = (uint32_t)((uint64_t)cus / big);
-  if (splits < 2 || splits > 6 || big * splits * 5 < (uint64_t)cus * 4) return c;
-  return {kBig, splits};
+  if (q.m > 128 && (uint64_t)k * (pairs ? 3 : 1) >= kSplitWork && splits >= 2 && splits <= 6 &&
+      big * splits * 5 >= (uint64_t)cus * 4)
+    return {kBig, splits};
+  if (c.shape == kMid) return c;
+  const uint64_t small = (uint64_t)triangle_tiles(q.m, 64) * nmat;
+  const uint32_t shares = (uint32_t)std::min<uint64_t>({2 * (uint64_t)cus / small, k / 512, 16});
+  return {kSmall, shares >= (pairs ? 2u : 3u) ? shares : 1};
 }
 
 template <DType T>
@@ -583,7 +592,8 @@ size_t ortho_space(const OrthoArgs& a) {
   size_t parts = 0;
   for (uint32_t k : {q.n, q.m}) {
     const Choice c = choose_sym(q, a.cus, a.nranks, k, pairs(a.type));
-    if (c.splits > 1) parts = std::max(parts, (size_t)c.splits * a.nranks * triangle_tiles(q.m, 256) * (256 * 256 * sizeof(float)));
+    const uint32_t b = c.shape == kBig ? 256 : 64;
+    if (c.splits > 1) parts = std::max(parts, (size_t)c.splits * a.nranks * triangle_tiles(q.m, b) * (b * b * sizeof(float)));
   }
   return align_up((size_t)a.nranks * q.parts * sizeof(double), 256) + (size_t)a.nranks * q.bytes + parts;
 }

@@ -373,7 +373,7 @@ def test_balance_loss_masked_rows():
 # --- orthogonalisation -------------------------------------------------------
 
 ORTHO = [(1, 1, 1), (2, 1, 9), (1, 9, 1), (3, 5, 4), (2, 64, 64), (1, 127, 130), (8, 128, 200), (2, 300, 129),
-         (1, 257, 513), (64, 24, 40), (1, 700, 650)]
+         (1, 257, 513), (64, 24, 40), (1, 700, 650), (3, 17, 7412), (1, 2500, 130)]
 
 
 def ortho_case(n, rows, cols, dtype, fade=True):
@@ -421,7 +421,7 @@ def test_orthogonalize(n, rows, cols, dtype):
 # step's), wide and tall, with rows of whole 16-byte vectors and without; long
 # ones, whose products are split along the sum.
 ORTHO_MANY = [(64, 130, 200), (64, 200, 300), (64, 300, 296), (64, 304, 296), (64, 296, 301), (64, 521, 520), (40, 40, 5504),
-              (40, 5501, 40), (40, 24, 16400)]
+              (40, 5501, 40), (40, 24, 16400), (40, 200, 5504), (40, 5500, 200)]
 
 
 @pytest.mark.parametrize("dtype", ["f32", "f16", "bf16"])
