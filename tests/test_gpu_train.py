@@ -541,6 +541,36 @@ def test_captured_graphs_replay():
             assert all(torch.equal(a, b) for a, b in zip(outputs(s), want)), f"replay {rep}"
 
 
+def test_captured_graph_of_few_tokens_and_long_matrices():
+    from double_binary_tree_amd import emucomm as E
+    announce("few tokens and a long matrix captured in a graph")
+    x, ws, _, y = xent_case([70, 50], 20, 64, "f16", 5)
+    long = ortho_case(2, 30, 3000, "f32")
+    loss, lse, d = (torch.full((20,), 0.3, device="cuda") for _ in range(3))
+    dx, dws, ups = torch.empty_like(x), [torch.empty_like(w) for w in ws], [torch.empty_like(g) for g in long]
+    work = [E.cross_entropy_workspace(x, ws), E.cross_entropy_workspace(x, ws, grad=True), E.orthogonalize_workspace(long)]
+
+    def once():
+        E.cross_entropy_tensors(x, ws, y, loss, lse, workspace=work[0])
+        E.cross_entropy_grad_tensors(x, ws, y, lse, d, dx, dws, workspace=work[1])
+        E.orthogonalize_tensors(long, ups, workspace=work[2])
+    outs = [loss, lse, dx, *dws, *ups]
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        once()
+    for rep in range(3):
+        x.mul_(-1.5 if rep else 1.0)
+        long[0].add_(0.25)
+        once()
+        want = [t.clone() for t in outs]
+        for t in outs + work:
+            t.zero_()
+        torch.cuda.synchronize()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(outs, want)), f"replay {rep}"
+
+
 def test_streams_of_their_own():
     from double_binary_tree_amd import emucomm as E
     announce("training-step operators on two streams at once")
